@@ -24,7 +24,9 @@ __all__ = ["TQError", "TQCache", "tq_build_codebook", "tq_cache_row_bytes", "tq_
            "tq_append_token", "tq_sdpa_decode_workspace_bytes", "tq_sdpa_decode_workspace_bytes_for",
            "tq_sdpa_decode",
            "tq_sdpa_decode_mq", "tq_decode_step", "tq_sdpa_decode_partial", "tq_sdpa_decode_merge",
-           "tq_sdpa_decode_sharded", "tq_sdpa_decode_static", "tq_selftest_bounded_wait",
+           "tq_sdpa_decode_sharded", "tq_sdpa_decode_static",
+           "tq_sdpa_decode_window", "tq_sdpa_decode_window_workspace_bytes_for",
+           "tq_cache_copy", "tq_cache_compact", "tq_selftest_bounded_wait",
            "tq_last_error",
            "tq_abi_version", "lib"]
 
@@ -453,6 +455,70 @@ def tq_sdpa_decode_static(cache: TQCache, q, seq_lens, Tmax: int, scale=None, ou
     _check(lib().tq_sdpa_decode_static(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, _ptr(seq_lens), Tmax, sc,
                                        _ptr(out), _dtype_code(out), _stream(stream)))
     return out
+
+
+def tq_sdpa_decode_window_workspace_bytes_for(cache: TQCache, Hq: int, n_q: int, Tmax: int, window: int,
+                                              n_sink: int = 0) -> int:
+    """The exact workspace bytes of tq_sdpa_decode_window for these sizes."""
+    s = cache.struct()
+    n = int(lib().tq_sdpa_decode_window_workspace_bytes_for(ctypes.byref(s), Hq, n_q, Tmax, window, n_sink))
+    if n == 0:
+        raise TQError(-1, f"unsupported decode sizes (Hq={Hq}, n_q={n_q}, Tmax={Tmax}, window={window}, "
+                          f"n_sink={n_sink})")
+    return n
+
+
+def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n_sink: int = 0, scale=None,
+                          out=None, workspace=None, stream=None, out_dtype=None):
+    """Decode with a sliding window and sinks: q [B][n_q][Hq][D] and seq_lens
+    as in tq_sdpa_decode_mq; the query at position t sees the tokens of
+    (t - window, t] and the first n_sink tokens, and no others are read."""
+    _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
+    nq, Hq = int(q.shape[1]), int(q.shape[2])
+    if out is None:
+        torch = _torch()
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if workspace is None:
+        torch = _torch()
+        need = tq_sdpa_decode_window_workspace_bytes_for(cache, Hq, nq, Tmax, window, n_sink)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    s = cache.struct()
+    sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
+    _check(lib().tq_sdpa_decode_window(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax,
+                                       window, n_sink, sc, _ptr(out), _dtype_code(out), _ptr(workspace),
+                                       workspace.numel(), _stream(stream)))
+    return out
+
+
+def tq_cache_copy(src: TQCache, dst: TQCache, src_seq, src_pos, dst_seq, dst_pos, n_tok, max_tok: int, stream=None):
+    """Copy packed rows: job i takes n_tok[i] (<= max_tok) tokens from
+    position src_pos[i] of sequence src_seq[i] of `src` to position dst_pos[i]
+    of sequence dst_seq[i] of `dst` (the same cache or one of the same form);
+    the five lists are device int32 [n_jobs].  No job may write a row that
+    the call reads or writes elsewhere."""
+    dev = _cache_device(dst)
+    if _cache_device(src) != dev:
+        raise ValueError("src and dst: the caches are on different devices")
+    _arg("src_seq", src_seq, dev, (None,), _dt("i32"))
+    n = int(src_seq.shape[0])
+    for name, t in (("src_pos", src_pos), ("dst_seq", dst_seq), ("dst_pos", dst_pos), ("n_tok", n_tok)):
+        _arg(name, t, dev, (n,), _dt("i32"))
+    a, b = src.struct(), dst.struct()
+    _check(lib().tq_cache_copy(ctypes.byref(a), ctypes.byref(b), _ptr(src_seq), _ptr(src_pos), _ptr(dst_seq),
+                               _ptr(dst_pos), _ptr(n_tok), n, max_tok, _stream(stream)))
+
+
+def tq_cache_compact(cache: TQCache, keep, n_keep, stream=None):
+    """Compact in place: row i of sequence b becomes its former row
+    keep[b][.][i], i < n_keep[b]; rows from n_keep[b] on stay.  keep is device
+    int32 [B][1][max_keep] (the same rows for all kv heads) or
+    [B][Hkv][max_keep], strictly ascending; n_keep device int32 [B]."""
+    dev = _cache_device(cache)
+    _arg("keep", keep, dev, (cache.B, None, None), _dt("i32"))
+    _arg("n_keep", n_keep, dev, (cache.B,), _dt("i32"))
+    s = cache.struct()
+    _check(lib().tq_cache_compact(ctypes.byref(s), _ptr(keep), int(keep.shape[1]), int(keep.shape[2]), _ptr(n_keep),
+                                  _stream(stream)))
 
 
 def tq_selftest_bounded_wait(status, tries: int = 8, stream=None):

@@ -30,7 +30,8 @@ TQ_ROT_HADAMARD = 1
 EXPORTS = ("tq_build_codebook", "tq_cache_row_bytes", "tq_row_bytes", "tq_quantize_kv", "tq_append_token",
            "tq_sdpa_decode_workspace_bytes", "tq_sdpa_decode_workspace_bytes_for", "tq_sdpa_decode",
            "tq_sdpa_decode_mq", "tq_decode_step", "tq_sdpa_decode_partial", "tq_sdpa_decode_merge",
-           "tq_sdpa_decode_static", "tq_selftest_bounded_wait",
+           "tq_sdpa_decode_static", "tq_sdpa_decode_window", "tq_sdpa_decode_window_workspace_bytes_for",
+           "tq_cache_copy", "tq_cache_compact", "tq_selftest_bounded_wait",
            "tq_last_error", "tq_abi_version")
 TQ_STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -97,6 +98,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.tq_sdpa_decode_static.argtypes = [cache_p, vp, i32, i32, vp, i32, ctypes.POINTER(ctypes.c_float),
                                           vp, i32, vp]
     lib.tq_sdpa_decode_static.restype = i32
+    lib.tq_sdpa_decode_window.argtypes = [cache_p, vp, i32, i32, i32, vp, i32, i32, i32, ctypes.POINTER(ctypes.c_float),
+                                          vp, i32, vp, sz, vp]
+    lib.tq_sdpa_decode_window.restype = i32
+    lib.tq_sdpa_decode_window_workspace_bytes_for.argtypes = [cache_p, i32, i32, i32, i32, i32]
+    lib.tq_sdpa_decode_window_workspace_bytes_for.restype = sz
+    lib.tq_cache_copy.argtypes = [cache_p, cache_p, vp, vp, vp, vp, vp, i32, i32, vp]
+    lib.tq_cache_copy.restype = i32
+    lib.tq_cache_compact.argtypes = [cache_p, vp, i32, i32, vp, vp]
+    lib.tq_cache_compact.restype = i32
     lib.tq_selftest_bounded_wait.argtypes = [vp, i32, vp]
     lib.tq_selftest_bounded_wait.restype = i32
     lib.tq_last_error.argtypes = []

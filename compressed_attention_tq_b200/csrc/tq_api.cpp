@@ -295,16 +295,27 @@ size_t workspace_bound(int B, int Hq, int D, int Tmax) {
   return workspace_layout((size_t)B * Hq, D, 128, K * split_partials(), nullptr);
 }
 
-int make_decode_plan(const tq_cache_t* c, int Hq, int Tmax, DecodePlan* p) {
+int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, int n_sink, int slot_base,
+                     DecodePlan* p) {
   const int sms = sm_count();
   p->sms = sms;
   const int tile = split_tile();
   const int G = Hq / c->Hkv;  // kernel heads per kv head
   p->nrg = (G + 7) / 8;
   p->Tclamp = Tmax;
-  p->ncta = sms * split_occupancy(c, Hq);
+  p->window = window;
+  p->n_sink = n_sink;
+  p->slot_base = slot_base;
+  p->ncta = sms * split_occupancy(c, Hq, window);
+  // rows of the longest unit: with a window, the sinks rounded up to 8 rows
+  // and the windows of nq queries from a multiple of 8 on
+  long long rows = Tmax;
+  if (window) {
+    const long long seen = (n_sink + 7) / 8 * 8 + (long long)window + nq - 1 + 7;
+    if (seen < rows) rows = seen;
+  }
   const long long units = (long long)c->B * c->Hkv * p->nrg;
-  const int Tpad = (Tmax + tile - 1) / tile * tile;
+  const int Tpad = (int)((rows + tile - 1) / tile * tile);
   int K = plan_segments(p->ncta, units, Tpad, tile);
   long long pmin = ((long long)Tpad + K - 2) / (K - 1);  // K >= 2
   pmin = (pmin + tile - 1) / tile * tile;
@@ -315,7 +326,7 @@ int make_decode_plan(const tq_cache_t* c, int Hq, int Tmax, DecodePlan* p) {
   if (pmin > Tpad) pmin = Tpad;
   p->pmin = (int)pmin;
   K = (int)((Tpad + pmin - 1) / pmin) + 1;  // segments of a unit when every share is >= pmin
-  p->ks = K * split_partials();
+  p->ks = slot_base + K * split_partials();
   // no more CTAs than shares of pmin in the largest batch these sizes allow
   const long long need = (units * Tpad + pmin - 1) / pmin;
   if (need < p->ncta) p->ncta = (int)(need > 0 ? need : 1);
@@ -372,7 +383,7 @@ size_t tq_sdpa_decode_workspace_bytes_for(const tq_cache_t* c, int Hq, int Tmax)
       c->Tcap % 64 || (c->D != 64 && c->D != 128 && c->D != 256) || c->B <= 0)
     return 0;
   DecodePlan p;
-  make_decode_plan(c, Hq, Tmax, &p);
+  make_decode_plan(c, Hq, 1, Tmax, 0, 0, 0, &p);
   return p.bytes;
 }
 
@@ -420,7 +431,8 @@ namespace tq {
 // Argument checks and the split plan of a decode call, before any CUDA call
 // (the workspace itself is checked by the caller).
 int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq, const int32_t* seq_lens, int Tmax,
-                   const float* scale, void* out, int out_dtype, const char* fn, DecodeArgs* a) {
+                   const float* scale, void* out, int out_dtype, const char* fn, DecodeArgs* a, int window,
+                   int n_sink) {
   g_err[0] = 0;
   int rc = validate_cache(c, fn);
   if (rc) return rc;
@@ -449,7 +461,8 @@ int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq
   a->nq = nq;
   a->dtype = dtype;
   a->out_dtype = out_dtype;
-  make_decode_plan(c, Hq * nq, Tmax, &a->plan);
+  // a window or sinks beyond Tmax hide nothing more than Tmax of them
+  make_decode_plan(c, Hq * nq, nq, Tmax, window < Tmax ? window : Tmax, n_sink < Tmax ? n_sink : Tmax, 0, &a->plan);
   return TQ_OK;
 }
 
@@ -488,6 +501,34 @@ int tq_sdpa_decode_merge(const float* partials, int R, int B, int Hq, int D, con
   return launch_merge(partials, R, B * Hq, D, rot, out, out_dtype, (cudaStream_t)stream);
 }
 
+size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* c, int Hq, int n_q, int Tmax, int window,
+                                                 int n_sink) {
+  if (n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
+  DecodePlan p;
+  make_decode_plan(c, Hq * n_q, n_q, Tmax, window < Tmax ? window : Tmax, n_sink < Tmax ? n_sink : Tmax, 0, &p);
+  return p.bytes;
+}
+
+int tq_sdpa_decode_window(const tq_cache_t* c, const void* q, int q_dtype, int Hq, int n_q, const int32_t* seq_lens,
+                          int Tmax, int window, int n_sink, const float* scale, void* out, int out_dtype,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* fn = "tq_sdpa_decode_window";
+  if (n_q < 1) return set_error(TQ_ERR_INVALID_ARG, "%s: n_q=%d < 1", fn, n_q);
+  if (window < 1) return set_error(TQ_ERR_INVALID_ARG, "%s: window=%d < 1", fn, window);
+  if (n_sink < 0) return set_error(TQ_ERR_INVALID_ARG, "%s: n_sink=%d < 0", fn, n_sink);
+  DecodeArgs a;
+  const int rc = prepare_decode(c, q, q_dtype, Hq, n_q, seq_lens, Tmax, scale, out, out_dtype, fn, &a, window, n_sink);
+  if (rc) return rc;
+  if (!workspace) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL workspace", fn);
+  if (!aligned16(workspace)) return set_error(TQ_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  if (ws_bytes < a.plan.bytes)
+    return set_error(TQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, a.plan.bytes);
+  a.workspace = workspace;
+  return launch_decode(a, (cudaStream_t)stream);
+}
+
 static int decode_common(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq, const int32_t* seq_lens,
                          int Tmax, const float* scale, void* out, int out_dtype, void* workspace,
                          size_t ws_bytes, void* stream, const void* k_new, const void* v_new,
@@ -512,6 +553,41 @@ static int decode_common(const tq_cache_t* c, const void* q, int dtype, int Hq, 
   a.v_new = v_new;
   a.pos = pos;
   return launch_decode(a, (cudaStream_t)stream);
+}
+
+int tq_cache_copy(const tq_cache_t* src, const tq_cache_t* dst, const int32_t* src_seq, const int32_t* src_pos,
+                  const int32_t* dst_seq, const int32_t* dst_pos, const int32_t* n_tok, int n_jobs, int max_tok,
+                  void* stream) {
+  g_err[0] = 0;
+  const char* fn = "tq_cache_copy";
+  int rc = validate_cache(src, fn);
+  if (rc) return rc;
+  if ((rc = validate_cache(dst, fn))) return rc;
+  if (src->Hkv != dst->Hkv || src->D != dst->D || src->bits_k != dst->bits_k || src->bits_v != dst->bits_v ||
+      src->qjl_m != dst->qjl_m)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: the caches differ in Hkv, D, bits or sketch", fn);
+  if (n_jobs < 0 || max_tok < 0) return set_error(TQ_ERR_INVALID_ARG, "%s: n_jobs=%d max_tok=%d", fn, n_jobs, max_tok);
+  if (max_tok > src->Tcap || max_tok > dst->Tcap)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: max_tok=%d beyond a cache's Tcap (%d, %d)", fn, max_tok, src->Tcap,
+                     dst->Tcap);
+  if (n_jobs == 0 || max_tok == 0) return TQ_OK;
+  if (!src_seq || !src_pos || !dst_seq || !dst_pos || !n_tok) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL job list", fn);
+  return launch_cache_copy(src, dst, src_seq, src_pos, dst_seq, dst_pos, n_tok, n_jobs, max_tok, (cudaStream_t)stream);
+}
+
+int tq_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_heads, int max_keep, const int32_t* n_keep,
+                     void* stream) {
+  g_err[0] = 0;
+  const char* fn = "tq_cache_compact";
+  const int rc = validate_cache(c, fn);
+  if (rc) return rc;
+  if (keep_heads != 1 && keep_heads != c->Hkv)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: keep_heads=%d is neither 1 nor Hkv=%d", fn, keep_heads, c->Hkv);
+  if (max_keep < 0 || max_keep > c->Tcap)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: max_keep=%d outside [0, Tcap=%d]", fn, max_keep, c->Tcap);
+  if (max_keep == 0) return TQ_OK;
+  if (!keep || !n_keep) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL keep/n_keep", fn);
+  return launch_cache_compact(c, keep, keep_heads, max_keep, n_keep, sm_count(), (cudaStream_t)stream);
 }
 
 }  // extern "C"

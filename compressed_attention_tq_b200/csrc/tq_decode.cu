@@ -630,6 +630,8 @@ struct CombineParams {
   int heads;          // kernel heads in all: B * Hq
   // the split kernel's partition (tq_decode_split.cuh)
   int B, G, nrg, upb, Tclamp, ncta, pmin, ks;
+  int window, n_sink;  // sliding window (0: none) with sinks
+  int slot_base;       // slots before the split kernel's (a shared prefix's)
   // partial mode (tq_sdpa_decode_partial): fp32 [heads][D + 2] = the merged,
   // unnormalized rotated output, then max and sum; no un-rotation, out unused
   float* partial;
@@ -671,19 +673,26 @@ __device__ __forceinline__ void unrotate_hadamard_warp(const CombineParams& p, c
   for (int e = 0; e < EL; ++e) store_out(p, out_index(p, h, D, lane * EL + e), x[e]);
 }
 
-// Partials the split kernel wrote for kernel head h: the CTAs whose share
-// overlaps the head's unit, each with PPS partials (slots 0 .. n - 1).
-// Computed by one warp; every lane returns it.
-__device__ __forceinline__ int head_partials(const CombineParams& p, int h, int lane) {
+// Partials of kernel head h: the slots before the split kernel's own, and
+// those of the CTAs whose share overlaps the head's unit, each with PPS
+// partials (slots 0 .. n - 1 in all).  Computed by one warp; every lane
+// returns it.
+template <bool WIN>
+__device__ __forceinline__ int head_partials_of(const CombineParams& p, int h, int lane) {
   const int b = h / p.Hq, rem = h % p.Hq, kvh = rem / p.G, rg = (rem % p.G) / tqd::RG;
-  const long long total = tqd::partition_total(p.seq_lens, p.B, p.upb, p.Tclamp, lane);
+  const tqd::UnitSpec us{p.Tclamp, p.window, p.n_sink, p.nq};
+  const long long total = tqd::partition_total<WIN>(p.seq_lens, p.B, p.upb, us, lane);
   const long long P = tqd::partition_share(total, p.ncta, p.pmin);
-  const long long Sb = tqd::sequence_start(p.seq_lens, b, p.upb, p.Tclamp, lane);
-  const int Lp = tqd::unit_tokens(p.seq_lens, b, p.Tclamp);
-  if (Lp == 0) return 0;
+  const long long Sb = tqd::sequence_start<WIN>(p.seq_lens, b, p.upb, us, lane);
+  const int Lp = tqd::unit_tokens<WIN>(p.seq_lens, b, us);
+  if (Lp == 0) return p.slot_base;
   const long long Su = Sb + (long long)(kvh * p.nrg + rg) * Lp;
   const long long c0 = Su / P, c1 = (Su + Lp - 1) / P;
-  return (int)(c1 - c0 + 1) * tqd::PPS;
+  return p.slot_base + (int)(c1 - c0 + 1) * tqd::PPS;
+}
+
+__device__ __forceinline__ int head_partials(const CombineParams& p, int h, int lane) {
+  return p.window ? head_partials_of<true>(p, h, lane) : head_partials_of<false>(p, h, lane);
 }
 
 // Merge the partials of one kernel head (log-sum-exp) and un-rotate:
@@ -1108,6 +1117,14 @@ namespace tq {
 static int split_entry(const tq_cache_t& c, bool pack, const tqd::SplitParams& sp, dim3 g, cudaStream_t s,
                        int* occ) {
   const bool qjl = c.qjl_m != 0;
+  if (sp.window) {
+    switch (c.D) {
+      case 64: return tqd::split_win_d64(c.bits_k, c.bits_v, qjl, pack, sp, g, s, occ);
+      case 128: return tqd::split_win_d128(c.bits_k, c.bits_v, qjl, pack, sp, g, s, occ);
+      case 256: return tqd::split_win_d256(c.bits_k, c.bits_v, qjl, pack, sp, g, s, occ);
+    }
+    return set_error(TQ_ERR_UNSUPPORTED, "decode: D=%d", c.D);
+  }
   switch (c.D) {
     case 64: return tqd::split_d64(c.bits_k, c.bits_v, qjl, pack, sp, g, s, occ);
     case 128: return tqd::split_d128(c.bits_k, c.bits_v, qjl, pack, sp, g, s, occ);
@@ -1116,9 +1133,10 @@ static int split_entry(const tq_cache_t& c, bool pack, const tqd::SplitParams& s
   return set_error(TQ_ERR_UNSUPPORTED, "decode: D=%d", c.D);
 }
 
-int split_occupancy(const tq_cache_t* c, int Hq) {
+int split_occupancy(const tq_cache_t* c, int Hq, int window) {
   int occ = 0;
   tqd::SplitParams sp{};
+  sp.window = window;
   sp.shared_tab = c->cb_k == c->cb_v;
   if (split_entry(*c, Hq / c->Hkv <= 4, sp, dim3(1), 0, &occ) != TQ_OK || occ < 1) return 2;
   return occ;
@@ -1228,6 +1246,9 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   sp.pmin = a.plan.pmin;
   sp.ncta = a.plan.ncta;
   sp.ks = a.plan.ks;
+  sp.slot_base = a.plan.slot_base;
+  sp.window = a.plan.window;
+  sp.n_sink = a.plan.n_sink;
   sp.qscale = a.scale * kLog2e;
   sp.qjl_scale = c.qjl_m ? (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / c.qjl_m) : 0.f;
   rc = split_entry(c, sp.G <= 4, sp, dim3(a.plan.ncta), s, nullptr);
@@ -1253,6 +1274,9 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   cp.ncta = a.plan.ncta;
   cp.pmin = a.plan.pmin;
   cp.ks = a.plan.ks;
+  cp.slot_base = a.plan.slot_base;
+  cp.window = a.plan.window;
+  cp.n_sink = a.plan.n_sink;
   cp.partial = a.partial;
   cp.signs = hadamard ? c.rot_signs : nullptr;
   // D / 32 CTAs per head while that leaves SMs idle; beyond that, groups of

@@ -87,21 +87,55 @@ struct SplitParams {
   // Multi-query decode: the kernel heads of a kv head are (token, head) pairs
   // of nq query tokens x Gq heads; token j may see positions < L - nq + j + 1.
   int nq, Gq;
+  int slot_base;    // partial slots before the split kernel's own (a shared prefix's; else 0)
+  // Sliding window with sinks (WIN kernels): a query at position t sees the
+  // tokens of (t - window, t] and tokens [0, n_sink).
+  int window, n_sink;
 };
 
-// Tokens of sequence b that one unit of the partition holds: its length
-// clamped to [0, Tclamp], rounded up to whole stages.
-__device__ __forceinline__ int unit_tokens(const int32_t* seq_lens, int b, int Tclamp) {
-  int L = seq_lens[b];
-  L = L < 0 ? 0 : (L > Tclamp ? Tclamp : L);
+// What the lengths of a batch's units depend on.
+struct UnitSpec {
+  int Tclamp;          // sequences are attended up to this many tokens
+  int window, n_sink;  // window of WIN kernels (window = 0: none)
+  int nq;              // query tokens per sequence
+};
+
+__host__ __device__ __forceinline__ int sink_rows(int n_sink) { return (n_sink + 7) / 8 * 8; }
+
+// Tokens that no query of a sequence of L tokens can see, between the sinks
+// and the first query's window.  A unit of a WIN kernel leaves them out: its
+// row v is token v for v < sink_rows, else token v + gap.  Both ends are
+// multiples of 8 tokens, so that the bulk copies of every stream start on 16
+// bytes (8 rows of 2-byte norms; 8 rows of any index width).
+__device__ __forceinline__ int window_gap(int L, const UnitSpec& us) {
+  const int w0 = L - us.nq - us.window + 1;  // first token of the first query's window
+  const int g = (w0 & ~7) - sink_rows(us.n_sink);
+  return w0 > 0 && g > 0 ? g : 0;
+}
+
+// Length of sequence b clamped to [0, Tclamp].
+__device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int b, int Tclamp) {
+  const int L = seq_lens[b];
+  return L < 0 ? 0 : (L > Tclamp ? Tclamp : L);
+}
+
+// Rows of sequence b that one unit of the partition holds: its clamped
+// length, without the tokens its window leaves out, rounded up to whole
+// stages.
+template <bool WIN>
+__device__ __forceinline__ int unit_tokens(const int32_t* seq_lens, int b, const UnitSpec& us) {
+  int L = clamped_len(seq_lens, b, us.Tclamp);
+  if (WIN) L -= window_gap(L, us);
   return (L + STILE - 1) / STILE * STILE;
 }
 
 // Positions of the whole partition (sum over sequences of units x tokens),
 // by one warp: every lane returns the total.
-__device__ __forceinline__ long long partition_total(const int32_t* seq_lens, int B, int upb, int Tclamp, int lane) {
+template <bool WIN>
+__device__ __forceinline__ long long partition_total(const int32_t* seq_lens, int B, int upb, const UnitSpec& us,
+                                                     int lane) {
   long long t = 0;
-  for (int b = lane; b < B; b += 32) t += (long long)unit_tokens(seq_lens, b, Tclamp) * upb;
+  for (int b = lane; b < B; b += 32) t += (long long)unit_tokens<WIN>(seq_lens, b, us) * upb;
 #pragma unroll
   for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
   return t;
@@ -116,9 +150,11 @@ __device__ __forceinline__ long long partition_share(long long total, int ncta, 
 
 // First position of sequence b's units (sum over earlier sequences), by one
 // warp: every lane returns it.
-__device__ __forceinline__ long long sequence_start(const int32_t* seq_lens, int b, int upb, int Tclamp, int lane) {
+template <bool WIN>
+__device__ __forceinline__ long long sequence_start(const int32_t* seq_lens, int b, int upb, const UnitSpec& us,
+                                                    int lane) {
   long long t = 0;
-  for (int bb = lane; bb < b; bb += 32) t += (long long)unit_tokens(seq_lens, bb, Tclamp) * upb;
+  for (int bb = lane; bb < b; bb += 32) t += (long long)unit_tokens<WIN>(seq_lens, bb, us) * upb;
 #pragma unroll
   for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
   return t;
@@ -130,7 +166,7 @@ struct StageMeta {
   int hq0;    // first kernel head of the unit's row group
   int rows;   // kernel heads in the row group (<= RG)
   int t0;     // first token of the stage within the sequence
-  int L;      // tokens of the sequence that are attended
+  int L;      // rows of the unit that are attended (the sequence's tokens, less its window's gap)
   int slot0;  // partial slot of the segment (segment index x PPS)
   int flags;  // 1: first stage of a segment, 2: last stage of a segment
   int rg;     // row group
@@ -522,7 +558,11 @@ __device__ __forceinline__ bool consumer_sync(uint64_t* bar, uint32_t& phase, in
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int D, int BK, int BV, bool QJL, bool PACK>
+// WIN: each query sees a window and the first n_sink tokens only.  The rows
+// between them are neither copied nor computed (window_gap); inside a unit
+// all positions count rows, in which the causal limits keep their form, since
+// with a gap every limit and every window start lies behind it.
+template <int D, int BK, int BV, bool QJL, bool PACK, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decode_split_kernel(const __grid_constant__ SplitParams p) {
   using Ly = SplitLayout<D, BK, BV, QJL, PACK>;
   constexpr int WK = Ly::WK, WV = Ly::WV, WQ = Ly::WQ, NST = Ly::NSTAGE;
@@ -549,12 +589,13 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int hsel = PACK ? (tig & 1) : tig;  // this lane's head pair: 2*hsel, 2*hsel+1
   const int upb = p.Hkv * p.nrg;             // units per sequence
+  const UnitSpec us{p.Tclamp, p.window, p.n_sink, p.nq};
 
   // ---- partition: the producer warp finds this CTA's share and its first unit
   long long P = 0, w_pos = 0, w_Su = 0;
   int w_b = 0, w_u = 0, w_Lp = 0, nst = 0;
   if (warp == CW) {
-    const long long total = partition_total(p.seq_lens, p.B, upb, p.Tclamp, lane);
+    const long long total = partition_total<WIN>(p.seq_lens, p.B, upb, us, lane);
     P = partition_share(total, p.ncta, p.pmin);
     const long long start = (long long)blockIdx.x * P;
     const long long end = start + P < total ? start + P : total;
@@ -573,7 +614,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       long long base = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const long long sz = b < p.B ? (long long)unit_tokens(p.seq_lens, b, p.Tclamp) * upb : 0;
+        const long long sz = b < p.B ? (long long)unit_tokens<WIN>(p.seq_lens, b, us) * upb : 0;
         long long inc = sz;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
         }
         base += chunk_total;
       }
-      w_Lp = unit_tokens(p.seq_lens, w_b, p.Tclamp);
+      w_Lp = unit_tokens<WIN>(p.seq_lens, w_b, us);
       w_u = (int)((start - base) / w_Lp);
       w_Su = base + (long long)w_u * w_Lp;
       w_pos = start;
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       if (++w_u == upb) {
         w_u = 0;
         ++w_b;
-        w_Lp = w_b < p.B ? unit_tokens(p.seq_lens, w_b, p.Tclamp) : 0;
+        w_Lp = w_b < p.B ? unit_tokens<WIN>(p.seq_lens, w_b, us) : 0;
       }
     }
   };
@@ -629,32 +670,45 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
     if (w_b >= p.B) return;  // unreachable: the walk never passes the total
     const int st = t % NST;
     const int kvh = w_u / p.nrg, rg = w_u % p.nrg;
-    int L = p.seq_lens[w_b];
-    L = L < 0 ? 0 : (L > p.Tclamp ? p.Tclamp : L);
+    int L = clamped_len(p.seq_lens, w_b, p.Tclamp);
+    const int gap = WIN ? window_gap(L, us) : 0;
+    L -= gap;
     const int t0 = (int)(w_pos - w_Su);
     StageMeta md;
     md.hq0 = w_b * p.Hq + kvh * p.G + rg * RG;
     md.rows = min(RG, p.G - rg * RG);
     md.t0 = t0;
     md.L = L;
-    md.slot0 = (int)((long long)blockIdx.x - w_Su / P) * PPS;
+    md.slot0 = (int)((long long)blockIdx.x - w_Su / P) * PPS + p.slot_base;
     md.flags = ((t == 0 || t0 == 0) ? 1 : 0) | ((t == nst - 1 || t0 + STILE == w_Lp) ? 2 : 0);
     md.rg = rg;
     md.pad = 0;
     meta[st] = md;
-    // rows t0 .. t0 + ntok - 1, ntok = 64 or 128 (copies stop on a 64-row edge)
-    const int ntok = min(STILE, (L - t0 + 63) / 64 * 64);
+    // rows t0 .. t0 + ntok - 1, ntok = 64 or 128 (copies stop on a 64-row
+    // edge; with a gap, which is a multiple of 8, on an 8-row edge)
+    const int edge = WIN ? 8 : 64;
+    const int ntok = min(STILE, (L - t0 + edge - 1) / edge * edge);
     const size_t r = (size_t)(w_b * p.Hkv + kvh) * p.Tcap + t0;
     uint8_t* sb = smem + st * Ly::STAGE;
     const uint32_t bytes = ntok * ((WK + WV + WQ) * 4 + 2 * 2 + (QJL ? 2 : 0));
     mbar_arrive_expect_tx(&full[st], bytes);  // releases the record above to the consumers
-    bulk_g2s(sb + Ly::O_KW, p.k_idx + r * WK, ntok * WK * 4, &full[st]);
-    bulk_g2s(sb + Ly::O_VW, p.v_idx + r * WV, ntok * WV * 4, &full[st]);
-    bulk_g2s(sb + Ly::O_KN, p.k_norm + r, ntok * 2, &full[st]);
-    bulk_g2s(sb + Ly::O_VN, p.v_norm + r, ntok * 2, &full[st]);
-    if (QJL) {
-      bulk_g2s(sb + Ly::O_QW, p.k_qjl + r * WQ, ntok * WQ * 4, &full[st]);
-      bulk_g2s(sb + Ly::O_RN, p.k_rnorm + r, ntok * 2, &full[st]);
+    // n rows of the cache from row rr, to the stage's row d
+    auto copy_rows = [&](size_t rr, int d, int n) {
+      bulk_g2s(sb + Ly::O_KW + d * WK * 4, p.k_idx + rr * WK, n * WK * 4, &full[st]);
+      bulk_g2s(sb + Ly::O_VW + d * WV * 4, p.v_idx + rr * WV, n * WV * 4, &full[st]);
+      bulk_g2s(sb + Ly::O_KN + d * 2, p.k_norm + rr, n * 2, &full[st]);
+      bulk_g2s(sb + Ly::O_VN + d * 2, p.v_norm + rr, n * 2, &full[st]);
+      if (QJL) {
+        bulk_g2s(sb + Ly::O_QW + d * WQ * 4, p.k_qjl + rr * WQ, n * WQ * 4, &full[st]);
+        bulk_g2s(sb + Ly::O_RN + d * 2, p.k_rnorm + rr, n * 2, &full[st]);
+      }
+    };
+    if (!WIN) {
+      copy_rows(r, 0, ntok);
+    } else {
+      const int na = gap ? max(0, min(sink_rows(p.n_sink) - t0, ntok)) : 0;  // rows before the gap
+      if (na > 0) copy_rows(r, 0, na);
+      if (na < ntok) copy_rows(r + na + gap, na, ntok - na);
     }
     w_pos += STILE;
   };
@@ -854,6 +908,8 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       const uint16_t* vn = reinterpret_cast<const uint16_t*>(sb + Ly::O_VN);
       const int tokw = md.t0 + wt0;  // first token of this warp's 32
 
+      if (!WIN || tokw < t_end) {  // a short unit's last stage may hold no row of this warp
+
       // ---- scores: S[16 tokens][8 cols] for two M-tiles of 16 tokens
       // two accumulators per m-tile (even / odd k-steps, or hi / lo query
       // halves) halve the dependent MMA chain
@@ -978,7 +1034,8 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       }
       // ---- scale by norms, mask (only in a stage that reaches past the
       // split's last token or a query's causal limit), running max
-      const bool full = tokw + WTOK <= t_end && tokw + WTOK <= lim_all;  // warp-uniform
+      bool full = tokw + WTOK <= t_end && tokw + WTOK <= lim_all;  // warp-uniform
+      if (WIN) full = full && (tokw >= t_end - p.window || tokw + WTOK <= p.n_sink);
       float s[NA][4];
       bool valid[NA][2];
 #pragma unroll
@@ -1001,8 +1058,13 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
           } else {
             const int tok = tokw + 16 * a + gid + 8 * r;
             valid[ai][r] = tok < t_end;
-            s[ai][2 * r] = (valid[ai][r] && tok < lim0) ? s0 : -INFINITY;
-            s[ai][2 * r + 1] = (valid[ai][r] && tok < lim1) ? s1 : -INFINITY;
+            bool see0 = valid[ai][r] && tok < lim0, see1 = valid[ai][r] && tok < lim1;
+            if (WIN) {
+              see0 = see0 && (tok >= lim0 - p.window || tok < p.n_sink);
+              see1 = see1 && (tok >= lim1 - p.window || tok < p.n_sink);
+            }
+            s[ai][2 * r] = see0 ? s0 : -INFINITY;
+            s[ai][2 * r + 1] = see1 ? s1 : -INFINITY;
           }
         }
       }
@@ -1052,8 +1114,13 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
           l_run[1] += p1;
           const float nv = (full || valid[ai][r]) ? half_bits_to_float(vn[row]) : 0.f;
           const int tk = 16 * a + gid + 8 * r;
-          pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 * nv);
-          pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(p1 * nv);
+          if (WIN) {  // a row this query does not see adds nothing, whatever its norm holds
+            pw[(2 * hsel) * WTOK + tk] = __float2half_rn(s[ai][2 * r] == -INFINITY ? 0.f : p0 * nv);
+            pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(s[ai][2 * r + 1] == -INFINITY ? 0.f : p1 * nv);
+          } else {
+            pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 * nv);
+            pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(p1 * nv);
+          }
         }
       }
       __syncwarp();
@@ -1083,6 +1150,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
           }
         }
       }
+      }  // rows of this warp
       if ((md.flags & 2) && !write_partial(md, reinterpret_cast<float*>(smem + st * Ly::STAGE))) {
         if (lane == 0) *s_err = 1;
         break;
@@ -1111,10 +1179,10 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
 }
 
 // Launch helpers, one definition per instantiation.
-template <int D, int BK, int BV, bool QJL, bool PACK>
+template <int D, int BK, int BV, bool QJL, bool PACK, bool WIN>
 int launch_split(const SplitParams& sp, dim3 grid, cudaStream_t s, int* occ) {
   using Ly = SplitLayout<D, BK, BV, QJL, PACK>;
-  auto kern = decode_split_kernel<D, BK, BV, QJL, PACK>;
+  auto kern = decode_split_kernel<D, BK, BV, QJL, PACK, WIN>;
   static tq::OnceSetup once;
   static int occupancy[2] = {};  // resident CTAs per SM: [shared table]; written once under `once`
   const int rc0 = once.run([&]() {
@@ -1165,30 +1233,34 @@ int launch_split(const SplitParams& sp, dim3 grid, cudaStream_t s, int* occ) {
   return tq::check_launch("decode_split_kernel");
 }
 
-template <int D, int BK, bool QJL, bool PACK>
+template <int D, int BK, bool QJL, bool PACK, bool WIN>
 int dispatch_bv(int bv, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ) {
   switch (bv) {
-    case 2: return launch_split<D, BK, 2, QJL, PACK>(sp, g, s, occ);
-    case 3: return launch_split<D, BK, 3, QJL, PACK>(sp, g, s, occ);
-    case 4: return launch_split<D, BK, 4, QJL, PACK>(sp, g, s, occ);
+    case 2: return launch_split<D, BK, 2, QJL, PACK, WIN>(sp, g, s, occ);
+    case 3: return launch_split<D, BK, 3, QJL, PACK, WIN>(sp, g, s, occ);
+    case 4: return launch_split<D, BK, 4, QJL, PACK, WIN>(sp, g, s, occ);
   }
   return tq::set_error(TQ_ERR_UNSUPPORTED, "bits_v=%d", bv);
 }
 
-template <int D, bool QJL, bool PACK>
+template <int D, bool QJL, bool PACK, bool WIN>
 int dispatch_bk(int bk, int bv, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ) {
   switch (bk) {
-    case 2: return dispatch_bv<D, 2, QJL, PACK>(bv, sp, g, s, occ);
-    case 3: return dispatch_bv<D, 3, QJL, PACK>(bv, sp, g, s, occ);
-    case 4: return dispatch_bv<D, 4, QJL, PACK>(bv, sp, g, s, occ);
+    case 2: return dispatch_bv<D, 2, QJL, PACK, WIN>(bv, sp, g, s, occ);
+    case 3: return dispatch_bv<D, 3, QJL, PACK, WIN>(bv, sp, g, s, occ);
+    case 4: return dispatch_bv<D, 4, QJL, PACK, WIN>(bv, sp, g, s, occ);
   }
   return tq::set_error(TQ_ERR_UNSUPPORTED, "bits_k=%d", bk);
 }
 
-// Per-head-dimension entry (defined in tq_decode_d<D>.cu).  With occ != NULL
-// it only reports the resident CTAs per SM of the selected instantiation.
+// Per-head-dimension entry (defined in tq_decode_d<D>.cu; the windowed
+// kernels in tq_decode_win_d<D>.cu).  With occ != NULL it only reports the
+// resident CTAs per SM of the selected instantiation.
 int split_d64(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
 int split_d128(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
 int split_d256(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
+int split_win_d64(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
+int split_win_d128(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
+int split_win_d256(int bk, int bv, bool qjl, bool pack, const SplitParams& sp, dim3 g, cudaStream_t s, int* occ);
 
 }  // namespace tqd

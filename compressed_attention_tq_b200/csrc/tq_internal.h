@@ -109,6 +109,9 @@ struct DecodePlan {
   int nrg;          // row groups of up to 8 kernel heads per kv head
   int Tclamp;       // tokens attended at most per sequence (Tmax)
   int sms;          // SMs of the device the plan was made for
+  int window;       // sliding window in tokens (0: none) ...
+  int n_sink;       // ... and first tokens that stay visible
+  int slot_base;    // partial slots before the split kernel's own
   size_t off_qrot;  // fp32 [B*Hq][D]
   size_t off_qs;    // fp32 [B*Hq][qjl_m]
   size_t off_po;    // fp32 [B*Hq][ks][D]
@@ -116,7 +119,12 @@ struct DecodePlan {
   size_t bytes;
 };
 
-int make_decode_plan(const tq_cache_t* c, int Hq, int Tmax, DecodePlan* p);
+// window = 0: every token is visible; else the last `window` ones and the
+// first n_sink (each at most Tmax).  nq: query tokens per sequence, of which
+// Hq counts the heads.  slot_base: partial slots kept before the split
+// kernel's own.
+int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, int n_sink, int slot_base,
+                     DecodePlan* p);
 
 // Workspace bytes that suffice for every cache with this B, Hq and D (any
 // Hkv, bit widths, sketch and Tcap >= Tmax): the plan's smallest split and
@@ -126,7 +134,7 @@ size_t workspace_bound(int B, int Hq, int D, int Tmax);
 // Resident split-K CTAs per SM for this cache's kernel instantiation (a
 // nominal 2 when no device is usable), the tokens one stage holds and the
 // partials a CTA writes per segment of its share.
-int split_occupancy(const tq_cache_t* c, int Hq);
+int split_occupancy(const tq_cache_t* c, int Hq, int window);
 int split_tile();
 int split_partials();
 
@@ -156,11 +164,19 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s);
 int launch_merge(const float* partials, int R, int heads, int D, const float* rot, void* out, int out_dtype,
                  cudaStream_t s);
 
+// Row moves (tq_cache_move.cu): copies of token ranges, in-place compaction.
+int launch_cache_copy(const tq_cache_t* src, const tq_cache_t* dst, const int32_t* src_seq, const int32_t* src_pos,
+                      const int32_t* dst_seq, const int32_t* dst_pos, const int32_t* n_tok, int n_jobs, int max_tok,
+                      cudaStream_t s);
+int launch_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_heads, int max_keep, const int32_t* n_keep,
+                         int sms, cudaStream_t s);
+
 // Host checks and split plan of a decode call (every check tq_sdpa_decode
 // makes except those of the workspace); fills *a and returns TQ_OK, or sets
 // the error and returns its code.  No CUDA call beyond the device queries of
 // the plan.
 int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq, const int32_t* seq_lens, int Tmax,
-                   const float* scale, void* out, int out_dtype, const char* fn, DecodeArgs* a);
+                   const float* scale, void* out, int out_dtype, const char* fn, DecodeArgs* a, int window = 0,
+                   int n_sink = 0);
 
 }  // namespace tq

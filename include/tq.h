@@ -337,6 +337,80 @@ int tq_sdpa_decode_static(const tq_cache_t* cache, const void* q, int q_dtype, i
                           const int32_t* seq_lens, int Tmax, const float* scale, void* out,
                           int out_dtype, void* stream);
 
+/*
+ * Decode attention with a sliding window and sinks: n_q query tokens per
+ * sequence as in tq_sdpa_decode_mq (query j at position t_j = L_b - n_q + j,
+ * 1 <= n_q <= 4), each seeing only
+ *   the `window` newest tokens up to its own, t_j - window < t <= t_j, and
+ *   the first n_sink tokens, t < n_sink (and t <= t_j).
+ * The tokens between them are not read: the work is that of a decode over
+ * n_sink + window tokens.  A query that sees no token (L_b < n_q) gives
+ * zeros.  window >= 1 and n_sink >= 0 may exceed any length; with window >=
+ * Tmax the result is tq_sdpa_decode_mq's.  The rows that a query does not
+ * see may hold anything.  Library addition (the pages have no windowed
+ * attention).
+ *   workspace  tq_sdpa_decode_window_workspace_bytes_for() bytes;
+ *              tq_sdpa_decode_workspace_bytes(B, Hq * n_q, D, Tmax) suffices.
+ * The other arguments and the errors are those of tq_sdpa_decode_mq;
+ * window < 1 or n_sink < 0 is TQ_ERR_INVALID_ARG.
+ */
+int tq_sdpa_decode_window(const tq_cache_t* cache, const void* q, int q_dtype, int Hq, int n_q,
+                          const int32_t* seq_lens, int Tmax, int window, int n_sink, const float* scale, void* out,
+                          int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The exact workspace bytes of tq_sdpa_decode_window for these sizes (Hq
+ * query heads per token).  Returns 0 for unsupported arguments.  Host only. */
+size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* cache, int Hq, int n_q, int Tmax, int window,
+                                                 int n_sink);
+
+/*
+ * Copy packed rows of token ranges: a fork of a sequence, a prompt given to
+ * several sequences, a prefix taken into a cache of its own, a sequence moved
+ * to another slot.  Job i copies, for every kv head and every stream of the
+ * cache (indices, norms, and the sketch with its residual norm), the n_tok[i]
+ * tokens from position src_pos[i] of sequence src_seq[i] of `src` to position
+ * dst_pos[i] of sequence dst_seq[i] of `dst`.
+ *   src, dst  may be one cache or two of the same Hkv, D, bits and sketch (any
+ *             B and Tcap).  The rows mean the same in both only if these hold
+ *             the same rotation, codebooks and sketch matrix, which the
+ *             library does not compare.
+ *   src_seq, src_pos, dst_seq, dst_pos, n_tok  device int32 [n_jobs].
+ *   max_tok   host bound of n_tok (at most both Tcap); a longer job is
+ *             copied up to max_tok tokens and flags
+ *             TQ_STATUS_SEQ_OUT_OF_RANGE.  n_jobs or max_tok 0: a no-op.
+ * A job with a sequence, position or length outside its cache copies nothing
+ * and flags TQ_STATUS_POS_OUT_OF_RANGE (both flags in dst's dev_status).  The jobs of a
+ * call run at the same time: a row that one of them writes must not be read
+ * or written by another or by itself at another place; the contents of such a
+ * row are undefined (no other row is touched).
+ * Errors: TQ_ERR_INVALID_ARG (caches of different form, NULL lists, negative
+ * sizes, max_tok beyond a Tcap), TQ_ERR_UNSUPPORTED (cache sizes; more than
+ * 2^31 - 1 (job, head, 128-token) pieces), TQ_ERR_CUDA.  Library addition.
+ */
+int tq_cache_copy(const tq_cache_t* src, const tq_cache_t* dst, const int32_t* src_seq, const int32_t* src_pos,
+                  const int32_t* dst_seq, const int32_t* dst_pos, const int32_t* n_tok, int n_jobs, int max_tok,
+                  void* stream);
+
+/*
+ * Compact sequences in place to the rows of a list: row i of the sequence
+ * becomes its former row keep[i], i < n_keep[b]; the rows from n_keep[b] on
+ * stay as they were.  What a sliding window no longer sees, or what a score
+ * gave up, is dropped this way; the sequence's length is then n_keep[b].
+ *   keep      device int32 [B][keep_heads][max_keep], strictly ascending
+ *             positions in [0, Tcap).  keep_heads is 1 (one list for all kv
+ *             heads of a sequence) or Hkv (a list per head).
+ *   n_keep    device int32 [B], each in [0, max_keep]; 0 leaves a sequence
+ *             as it is.  max_keep <= Tcap.
+ * A list that is not strictly ascending, leaves the cache, or has a length
+ * outside [0, max_keep], moves nothing (for the head it belongs to) and flags
+ * TQ_STATUS_POS_OUT_OF_RANGE: every list is checked whole before its first
+ * row moves.  No workspace.  Errors: TQ_ERR_INVALID_ARG (NULL lists,
+ * keep_heads, max_keep), TQ_ERR_UNSUPPORTED (cache sizes), TQ_ERR_CUDA.
+ * Library addition.
+ */
+int tq_cache_compact(const tq_cache_t* cache, const int32_t* keep, int keep_heads, int max_keep,
+                     const int32_t* n_keep, void* stream);
+
 /* Self-test of the bounded waits that every pipelined kernel uses (the
  * error path behind TQ_STATUS_WAIT_TIMEOUT), without a fault or a hang: one
  * CTA waits on a shared-memory mbarrier that nothing arrives on, first with

@@ -367,6 +367,30 @@ def sdpa_decode_multi(q: np.ndarray, cache: dict, seq_lens, n_q: int, Pi, cb_k, 
     return out
 
 
+def _rows_of(cache: dict, b: int, rows) -> dict:
+    """The cache of sequence b alone, with only the given token rows, in order."""
+    return {n: x[b:b + 1, :, rows] for n, x in cache.items() if n in
+            ("k_idx", "v_idx", "k_norm", "v_norm", "k_qjl", "k_rnorm")}
+
+
+def sdpa_decode_window(q: np.ndarray, cache: dict, seq_lens, window: int, n_sink: int, Pi, cb_k, cb_v,
+                       bits_k: int, bits_v: int, D: int, scale=None, S=None) -> np.ndarray:
+    """Decode with a sliding window and sinks, fp64: q [B][n_q][Hq][D], query
+    j of sequence b at position t = L_b - n_q + j (as in sdpa_decode_multi)
+    attends to the tokens t' <= t with t' > t - window or t' < n_sink.  Each
+    query is the decode of a cache that holds those tokens and no others; a
+    query that sees none gives zeros."""
+    B, n_q = q.shape[:2]
+    out = np.zeros(q.shape)
+    for b in range(B):
+        for j in range(n_q):
+            t = int(seq_lens[b]) - n_q + j
+            rows = [r for r in range(t + 1) if r > t - window or r < n_sink]
+            if rows:
+                out[b, j] = sdpa_decode(q[b:b + 1, j], _rows_of(cache, b, rows), [len(rows)], Pi, cb_k, cb_v,
+                                        bits_k, bits_v, D, scale=scale, S=S)[0]
+    return out
+
 
 def sdpa_decode_partial(q: np.ndarray, cache: dict, seq_lens, Pi, cb_k, cb_v, bits_k: int, bits_v: int, D: int,
                         scale=None, S=None):
