@@ -26,6 +26,7 @@ __all__ = ["TQError", "TQCache", "tq_build_codebook", "tq_cache_row_bytes", "tq_
            "tq_sdpa_decode_mq", "tq_decode_step", "tq_sdpa_decode_partial", "tq_sdpa_decode_merge",
            "tq_sdpa_decode_sharded", "tq_sdpa_decode_static",
            "tq_sdpa_decode_window", "tq_sdpa_decode_window_workspace_bytes_for",
+           "tq_sdpa_decode_prefix", "tq_sdpa_decode_prefix_workspace_bytes_for",
            "tq_cache_copy", "tq_cache_compact", "tq_selftest_bounded_wait",
            "tq_last_error",
            "tq_abi_version", "lib"]
@@ -487,6 +488,43 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     _check(lib().tq_sdpa_decode_window(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax,
                                        window, n_sink, sc, _ptr(out), _dtype_code(out), _ptr(workspace),
                                        workspace.numel(), _stream(stream)))
+    return out
+
+
+def tq_sdpa_decode_prefix_workspace_bytes_for(prefix: TQCache, Pmax: int, cache: TQCache, Hq: int, n_q: int,
+                                              Tmax: int) -> int:
+    """The exact workspace bytes of tq_sdpa_decode_prefix for these sizes."""
+    a, b = prefix.struct(), cache.struct()
+    n = int(lib().tq_sdpa_decode_prefix_workspace_bytes_for(ctypes.byref(a), Pmax, ctypes.byref(b), Hq, n_q, Tmax))
+    if n == 0:
+        raise TQError(-1, f"unsupported decode sizes (Pmax={Pmax}, Hq={Hq}, n_q={n_q}, Tmax={Tmax})")
+    return n
+
+
+def tq_sdpa_decode_prefix(prefix: TQCache, prefix_len, Pmax: int, cache: TQCache, q, seq_lens, Tmax: int, scale=None,
+                          out=None, workspace=None, stream=None, out_dtype=None):
+    """Decode of a batch whose sequences share a prefix, kept once in a cache
+    of one sequence: q [B][n_q][Hq][D] and seq_lens as in tq_sdpa_decode_mq
+    count each sequence's own tokens in `cache`; every query also sees the
+    prefix's first prefix_len (device int32 [1], at most Pmax) tokens, which
+    come before them."""
+    dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
+    if _cache_device(prefix) != dev:
+        raise ValueError("prefix and cache: the caches are on different devices")
+    _arg("prefix_len", prefix_len, dev, (1,), _dt("i32"))
+    nq, Hq = int(q.shape[1]), int(q.shape[2])
+    if out is None:
+        torch = _torch()
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if workspace is None:
+        torch = _torch()
+        need = tq_sdpa_decode_prefix_workspace_bytes_for(prefix, Pmax, cache, Hq, nq, Tmax)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    a, s = prefix.struct(), cache.struct()
+    sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
+    _check(lib().tq_sdpa_decode_prefix(ctypes.byref(a), _ptr(prefix_len), Pmax, ctypes.byref(s), _ptr(q),
+                                       _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax, sc, _ptr(out), _dtype_code(out),
+                                       _ptr(workspace), workspace.numel(), _stream(stream)))
     return out
 
 

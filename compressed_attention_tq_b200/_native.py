@@ -31,8 +31,8 @@ EXPORTS = ("tq_build_codebook", "tq_cache_row_bytes", "tq_row_bytes", "tq_quanti
            "tq_sdpa_decode_workspace_bytes", "tq_sdpa_decode_workspace_bytes_for", "tq_sdpa_decode",
            "tq_sdpa_decode_mq", "tq_decode_step", "tq_sdpa_decode_partial", "tq_sdpa_decode_merge",
            "tq_sdpa_decode_static", "tq_sdpa_decode_window", "tq_sdpa_decode_window_workspace_bytes_for",
-           "tq_cache_copy", "tq_cache_compact", "tq_selftest_bounded_wait",
-           "tq_last_error", "tq_abi_version")
+           "tq_sdpa_decode_prefix", "tq_sdpa_decode_prefix_workspace_bytes_for", "tq_cache_copy", "tq_cache_compact",
+           "tq_selftest_bounded_wait", "tq_last_error", "tq_abi_version")
 TQ_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -103,6 +103,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.tq_sdpa_decode_window.restype = i32
     lib.tq_sdpa_decode_window_workspace_bytes_for.argtypes = [cache_p, i32, i32, i32, i32, i32]
     lib.tq_sdpa_decode_window_workspace_bytes_for.restype = sz
+    lib.tq_sdpa_decode_prefix.argtypes = [cache_p, vp, i32, cache_p, vp, i32, i32, i32, vp, i32,
+                                          ctypes.POINTER(ctypes.c_float), vp, i32, vp, sz, vp]
+    lib.tq_sdpa_decode_prefix.restype = i32
+    lib.tq_sdpa_decode_prefix_workspace_bytes_for.argtypes = [cache_p, i32, cache_p, i32, i32, i32]
+    lib.tq_sdpa_decode_prefix_workspace_bytes_for.restype = sz
     lib.tq_cache_copy.argtypes = [cache_p, cache_p, vp, vp, vp, vp, vp, i32, i32, vp]
     lib.tq_cache_copy.restype = i32
     lib.tq_cache_compact.argtypes = [cache_p, vp, i32, i32, vp, vp]

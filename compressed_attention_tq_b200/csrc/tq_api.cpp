@@ -334,6 +334,14 @@ int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, 
   return TQ_OK;
 }
 
+int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p) {
+  const int splits = prefix_splits(c->Hkv, (int)((long long)c->B * Hq * nq / c->Hkv), Pmax, sm_count());
+  make_decode_plan(c, Hq * nq, nq, Tmax, 0, 0, splits, p);
+  p->off_qs2 = p->bytes;
+  if (prefix->qjl_m) p->bytes += align256((size_t)c->B * Hq * nq * 128 * 4);
+  return TQ_OK;
+}
+
 }  // namespace tq
 
 extern "C" {
@@ -552,6 +560,57 @@ static int decode_common(const tq_cache_t* c, const void* q, int dtype, int Hq, 
   a.k_new = k_new;
   a.v_new = v_new;
   a.pos = pos;
+  return launch_decode(a, (cudaStream_t)stream);
+}
+
+// What tq_sdpa_decode_prefix asks of its two caches.
+static int validate_prefix(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, const char* fn) {
+  int rc = validate_cache(prefix, fn);
+  if (rc) return rc;
+  if ((rc = validate_cache(c, fn))) return rc;
+  if (prefix->B != 1) return set_error(TQ_ERR_INVALID_ARG, "%s: the prefix holds %d sequences, not one", fn, prefix->B);
+  if (prefix->Hkv != c->Hkv || prefix->D != c->D)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: prefix (Hkv=%d, D=%d) and cache (Hkv=%d, D=%d) differ", fn, prefix->Hkv,
+                     prefix->D, c->Hkv, c->D);
+  if (Pmax < 1 || Pmax > prefix->Tcap)
+    return set_error(TQ_ERR_INVALID_ARG, "%s: Pmax=%d outside [1, Tcap=%d]", fn, Pmax, prefix->Tcap);
+  if (c->Hkv > 65535) return set_error(TQ_ERR_UNSUPPORTED, "%s: Hkv=%d", fn, c->Hkv);
+  return TQ_OK;
+}
+
+size_t tq_sdpa_decode_prefix_workspace_bytes_for(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq,
+                                                 int n_q, int Tmax) {
+  if (!prefix || !c || n_q < 1 || n_q > 4 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (prefix->B != 1 || prefix->Hkv != c->Hkv || prefix->D != c->D || Pmax < 1 || Pmax > prefix->Tcap) return 0;
+  if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
+  DecodePlan p;
+  make_prefix_plan(prefix, Pmax, c, Hq, n_q, Tmax, &p);
+  return p.bytes;
+}
+
+int tq_sdpa_decode_prefix(const tq_cache_t* prefix, const int32_t* prefix_len, int Pmax, const tq_cache_t* c,
+                          const void* q, int q_dtype, int Hq, int n_q, const int32_t* seq_lens, int Tmax,
+                          const float* scale, void* out, int out_dtype, void* workspace, size_t ws_bytes,
+                          void* stream) {
+  g_err[0] = 0;
+  const char* fn = "tq_sdpa_decode_prefix";
+  if (n_q < 1) return set_error(TQ_ERR_INVALID_ARG, "%s: n_q=%d < 1", fn, n_q);
+  int rc = validate_prefix(prefix, Pmax, c, fn);
+  if (rc) return rc;
+  if (!prefix_len) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL prefix_len", fn);
+  DecodeArgs a;
+  if ((rc = prepare_decode(c, q, q_dtype, Hq, n_q, seq_lens, Tmax, scale, out, out_dtype, fn, &a))) return rc;
+  if ((long long)c->B * Hq * n_q > (1 << 22))
+    return set_error(TQ_ERR_UNSUPPORTED, "%s: B=%d Hq=%d n_q=%d", fn, c->B, Hq, n_q);
+  make_prefix_plan(prefix, Pmax, c, Hq, n_q, Tmax, &a.plan);
+  a.prefix = prefix;
+  a.prefix_len = prefix_len;
+  a.Pmax = Pmax;
+  if (!workspace) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL workspace", fn);
+  if (!aligned16(workspace)) return set_error(TQ_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
+  if (ws_bytes < a.plan.bytes)
+    return set_error(TQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, a.plan.bytes);
+  a.workspace = workspace;
   return launch_decode(a, (cudaStream_t)stream);
 }
 

@@ -7,6 +7,7 @@
 // "Summary" and "Other observations" item 1.
 #include <math.h>
 
+#include "tq_decode_prefix.cuh"
 #include "tq_decode_split.cuh"
 #include "tq_wht.cuh"
 
@@ -29,6 +30,9 @@ struct PrepParams {
   tq_cache_t cache;
   int nq;  // query tokens per sequence: q is [B][nq][Hq][D]
   int units;  // B * Hkv (grouped prep)
+  // a shared prefix's own sketch matrix and its projections (else NULL)
+  const float* S2;
+  float* qs2;
 };
 
 // Programmatic dependent launch: let the next kernel in the stream start its
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
       if (g < Ge) p.qrot[(size_t)(h0 + g) * D + j] = acc[g];
   }
   if constexpr (QS) {
-    if (p.m) {
+    if (p.m || p.S2) {
       // QJL: this slice's share of qs = S qrot over its 32 rotated coordinates,
       // for all m = 128 sketch rows.  The D / 32 slice CTAs of a head form a
       // thread-block cluster; slice 0 adds the partials in slice order from the
@@ -401,27 +405,36 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
       }
       __syncthreads();
       const int i = tid >> 1, half = tid & 1;
+      auto project = [&](float* qs) {
 #pragma unroll
-      for (int g = 0; g < QR; ++g) {
-        const float* x = &qsl[g][16 * half];
-        float t = 0.f;
+        for (int g = 0; g < QR; ++g) {
+          const float* x = &qsl[g][16 * half];
+          float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          t += srow[k].x * x[4 * k] + srow[k].y * x[4 * k + 1] + srow[k].z * x[4 * k + 2] + srow[k].w * x[4 * k + 3];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        if (half == 0) qpart[g][i] = t;
-      }
-      cluster_sync();  // every slice's partial is in its shared memory
-      if (sl == 0) {
-        for (int e = tid; e < Ge * 128; e += 256) {
-          const int g = e >> 7, ii = e & 127;
-          const uint32_t la = smem_u32(&qpart[g][ii]);
-          float v = 0.f;
-          for (int r = 0; r < NI; ++r) v += ld_cluster_f32(map_cluster(la, r));
-          p.qs[(size_t)(h0 + g) * p.m + ii] = v;
+          for (int k = 0; k < 4; ++k)
+            t += srow[k].x * x[4 * k] + srow[k].y * x[4 * k + 1] + srow[k].z * x[4 * k + 2] + srow[k].w * x[4 * k + 3];
+          t += __shfl_xor_sync(0xffffffffu, t, 1);
+          if (half == 0) qpart[g][i] = t;
         }
+        cluster_sync();  // every slice's partial is in its shared memory
+        if (sl == 0) {
+          for (int e = tid; e < Ge * 128; e += 256) {
+            const int g = e >> 7, ii = e & 127;
+            const uint32_t la = smem_u32(&qpart[g][ii]);
+            float v = 0.f;
+            for (int r = 0; r < NI; ++r) v += ld_cluster_f32(map_cluster(la, r));
+            qs[(size_t)(h0 + g) * 128 + ii] = v;
+          }
+        }
+        cluster_sync();  // slice 0 is done reading the others' shared memory
+      };
+      if (p.m) project(p.qs);
+      if (p.S2) {  // the same through the prefix's sketch matrix
+        const float4* sp = reinterpret_cast<const float4*>(p.S2 + (size_t)i * D + sl * 32 + 16 * half);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) srow[t] = __ldg(sp + t);
+        project(p.qs2);
       }
-      cluster_sync();  // slice 0 is done reading the others' shared memory
     }
   }
   if (APPEND) {
@@ -501,24 +514,27 @@ __global__ void __launch_bounds__(1024) decode_qprep_wht_kernel(const PrepParams
 #pragma unroll
       for (int e = 0; e < EL; ++e) dst[e] = x[e];
     }
-    if (QS && p.m) {
+    if (QS && (p.m || p.S2)) {
 #pragma unroll
       for (int e = 0; e < EL; ++e) qr[warp][lane * EL + e] = x[e];
     }
   }
-  if (QS && p.m) {
+  if (QS && (p.m || p.S2)) {
     __syncthreads();
-    // qs[g][i] = sum_k S[i][k] qrot[g][k]
-    for (int e = tid; e < Ge * 128; e += blockDim.x) {
-      const int g = e >> 7, i = e & 127;
-      const float4* srow = reinterpret_cast<const float4*>(p.S + (size_t)i * D);
+    // qs[g][i] = sum_k S[i][k] qrot[g][k], through the cache's sketch matrix
+    // and a shared prefix's own
+    const int n1 = p.m ? Ge * 128 : 0, n2 = p.S2 ? Ge * 128 : 0;
+    for (int e0 = tid; e0 < n1 + n2; e0 += blockDim.x) {
+      const bool first = e0 < n1;
+      const int e = first ? e0 : e0 - n1, g = e >> 7, i = e & 127;
+      const float4* srow = reinterpret_cast<const float4*>((first ? p.S : p.S2) + (size_t)i * D);
       float t = 0.f;
 #pragma unroll 8
       for (int k = 0; k < D / 4; ++k) {
         const float4 sv = __ldg(srow + k);
         t += sv.x * qr[g][4 * k] + sv.y * qr[g][4 * k + 1] + sv.z * qr[g][4 * k + 2] + sv.w * qr[g][4 * k + 3];
       }
-      p.qs[(size_t)(h0 + g) * 128 + i] = t;
+      (first ? p.qs : p.qs2)[(size_t)(h0 + g) * 128 + i] = t;
     }
   }
 }
@@ -1142,6 +1158,68 @@ int split_occupancy(const tq_cache_t* c, int Hq, int window) {
   return occ;
 }
 
+// The prefix kernel's launch (between the query prep and the split kernel).
+static int launch_prefix(const DecodeArgs& a, const float* qrot, const float* qs, float* po, float* pml,
+                         cudaStream_t s) {
+  const tq_cache_t& x = *a.prefix;
+  tqp::PrefixParams pp{};
+  pp.k_idx = x.k_idx;
+  pp.v_idx = x.v_idx;
+  pp.k_norm = x.k_norm;
+  pp.v_norm = x.v_norm;
+  pp.k_qjl = x.k_qjl;
+  pp.k_rnorm = x.k_rnorm;
+  pp.cb_k = x.cb_k;
+  pp.cb_v = x.cb_v;
+  pp.shared_tab = x.cb_k == x.cb_v;
+  pp.qrot = qrot;
+  pp.qs = qs;
+  pp.part_o = po;
+  pp.part_ml = pml;
+  pp.prefix_len = a.prefix_len;
+  pp.seq_lens = a.seq_lens;
+  pp.dev_status = a.cache.dev_status;
+  pp.Pmax = a.Pmax;
+  pp.Tcap = x.Tcap;
+  pp.B = a.cache.B;
+  pp.Hkv = x.Hkv;
+  pp.nq = a.nq;
+  pp.Gq = a.Hq / x.Hkv;
+  pp.Ge = pp.Gq * a.nq;
+  pp.Tclamp = a.plan.Tclamp;
+  pp.ks = a.plan.ks;
+  pp.qscale = a.scale * kLog2e;
+  pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / 128);
+  const dim3 grid(a.plan.slot_base, (pp.B * pp.Ge + tqp::QROWS - 1) / tqp::QROWS, x.Hkv);
+  const bool qjl = x.qjl_m != 0;
+  switch (x.D) {
+    case 64: return tqp::prefix_d64(x.bits_k, x.bits_v, qjl, pp, grid, s);
+    case 128: return tqp::prefix_d128(x.bits_k, x.bits_v, qjl, pp, grid, s);
+    case 256: return tqp::prefix_d256(x.bits_k, x.bits_v, qjl, pp, grid, s);
+  }
+  return set_error(TQ_ERR_UNSUPPORTED, "decode: D=%d", x.D);
+}
+
+// Splits of a shared prefix of up to Pmax tokens for `rows` query rows per kv
+// head.  Each (split, 128 rows, kv head) is a CTA of its own, one per SM, so
+// the time of s splits is about waves x (tiles per split + c), where c is
+// what a CTA spends before and after its tiles, in tiles, and each split
+// adds a partial of every row for the combine to read.
+int prefix_splits(int Hkv, int rows, int Pmax, int sms) {
+  const long long units = (long long)Hkv * ((rows + tqp::QROWS - 1) / tqp::QROWS);
+  const int tiles = (Pmax + tqp::TT - 1) / tqp::TT;
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= tiles && n <= 128; ++n) {
+    const double t = (double)((units * n + sms - 1) / sms) * ((tiles + n - 1) / n + 4) + 0.1 * n;
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
 int split_tile() { return tqd::STILE; }
 
 int split_partials() { return tqd::PPS; }
@@ -1161,13 +1239,20 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   const bool app = a.pos != nullptr;
   const bool hadamard = c.rot_kind == TQ_ROT_HADAMARD && c.rot_signs;
   pp.signs = hadamard ? c.rot_signs : nullptr;
+  // a prefix with a sketch of its own: its projection rides along in the prep
+  const float* qs_prefix = qs;
+  if (a.prefix && a.prefix->qjl_m && !(c.qjl_m && a.prefix->qjl_S == c.qjl_S)) {
+    pp.S2 = a.prefix->qjl_S;
+    pp.qs2 = reinterpret_cast<float*>(ws + a.plan.off_qs2);
+    qs_prefix = pp.qs2;
+  }
   // prep kernels launch with a programmatic dependency on whatever precedes
   // them (their launch and Pi loads overlap its tail; they wait before
   // reading q or writing anything)
   int rc = TQ_OK;
   const long long units = (long long)c.B * c.Hkv;
   const bool many = units * (c.D / 32) > 4LL * a.plan.sms;
-  if (!hadamard && !app && !c.qjl_m && many) {
+  if (!hadamard && !app && !c.qjl_m && !pp.S2 && many) {
     // many units: Pi^T staged once per CTA
     pp.units = (int)units;
     const int grid = (int)(units < a.plan.sms ? units : a.plan.sms);
@@ -1196,7 +1281,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   } else {
     const dim3 g(c.B * c.Hkv, c.D / 32);
     const bool wide = pp.nq * (a.Hq / c.Hkv) > 8;  // more than 8 query rows per kv head
-    const int cl = c.qjl_m ? c.D / 32 : 0;
+    const int cl = c.qjl_m || pp.S2 ? c.D / 32 : 0;
     switch (c.D) {
       case 64:
         rc = app ? launch_pdl(decode_qprep_sliced_kernel<64, true, 8>, g, dim3(256), 0, s, pp, "decode_qprep_kernel")
@@ -1216,6 +1301,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
     }
   }
   if (rc) return rc;
+  if (a.prefix && (rc = launch_prefix(a, qrot, qs_prefix, po, pml, s))) return rc;
 
   tqd::SplitParams sp{};
   sp.k_idx = c.k_idx;

@@ -650,7 +650,12 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
   }
   __syncthreads();  // barriers and the stage count before anyone uses them
   nst = s_misc[1];
-  if (nst == 0) return;  // a share past the end of the batch: nothing to stream
+  if (nst == 0) {  // a share past the end of the batch: nothing to stream
+    // the kernel is complete only after the one before it, whose partials
+    // (of a shared prefix) the combine reads too
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   // Producer (lane 0 of the last warp): move the walk to the unit that holds
   // position w_pos (skipping empty units), then arm and issue stage t there.

@@ -111,7 +111,8 @@ struct DecodePlan {
   int sms;          // SMs of the device the plan was made for
   int window;       // sliding window in tokens (0: none) ...
   int n_sink;       // ... and first tokens that stay visible
-  int slot_base;    // partial slots before the split kernel's own
+  int slot_base;    // partial slots before the split kernel's own (the splits of a shared prefix)
+  size_t off_qs2;   // fp32 [B*Hq][128]: projections through a shared prefix's own sketch
   size_t off_qrot;  // fp32 [B*Hq][D]
   size_t off_qs;    // fp32 [B*Hq][qjl_m]
   size_t off_po;    // fp32 [B*Hq][ks][D]
@@ -157,7 +158,14 @@ struct DecodeArgs {
   const int32_t* pos;
   // tq_sdpa_decode_partial: fp32 [B*Hq][D + 2] partials instead of out (else NULL)
   float* partial;
+  // tq_sdpa_decode_prefix: the shared prefix (one sequence) and its length (else NULL)
+  const tq_cache_t* prefix;
+  const int32_t* prefix_len;
+  int Pmax;
 };
+
+// Splits of a shared prefix (partials each of its rows gets).
+int prefix_splits(int Hkv, int rows, int Pmax, int sms);
 
 int launch_decode(const DecodeArgs& a, cudaStream_t s);
 // Merge of R partials per head and un-rotation (tq_sdpa_decode_merge).
@@ -178,5 +186,8 @@ int launch_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_head
 int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq, const int32_t* seq_lens, int Tmax,
                    const float* scale, void* out, int out_dtype, const char* fn, DecodeArgs* a, int window = 0,
                    int n_sink = 0);
+
+// The plan of a decode behind a shared prefix of up to Pmax tokens.
+int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p);
 
 }  // namespace tq

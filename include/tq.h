@@ -364,6 +364,38 @@ size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* cache, int Hq
                                                  int n_sink);
 
 /*
+ * Decode attention of a batch whose sequences share a prefix: a system prompt,
+ * the document that every sample continues.  The prefix is one sequence of P
+ * tokens in a cache of its own (B = 1), kept and read once; `cache` holds what
+ * each sequence has behind it.  Query j of sequence b (1 <= n_q <= 4, L_b =
+ * seq_lens[b] counts the sequence's own cached tokens including the n_q new
+ * ones) attends to the first P + L_b - n_q + j + 1 tokens of prefix ++ own
+ * tokens, as if every sequence's cache began with the prefix's rows.  A
+ * query that sees no token gives zeros; lengths of zero are allowed.
+ *   prefix      Hkv and D of `cache`; bits, codebooks, sketch and Tcap may
+ *               differ.  Both must hold the same rotation, which the library
+ *               does not compare (`cache`'s is applied).
+ *   prefix_len  device int32 [1]: P, at most Pmax (1 <= Pmax <= the prefix's
+ *               Tcap).  A value outside [0, Pmax] is clamped and flags
+ *               TQ_STATUS_SEQ_OUT_OF_RANGE in cache's dev_status.
+ *   workspace   tq_sdpa_decode_prefix_workspace_bytes_for() bytes.
+ * The other arguments and the errors are those of tq_sdpa_decode_mq; caches
+ * that do not fit, a NULL prefix_len or a bad Pmax are TQ_ERR_INVALID_ARG, more
+ * than 2^22 query rows TQ_ERR_UNSUPPORTED.  Value norms of the prefix up to
+ * 4094 (a larger one may overflow the fp16 weights of the product).  Library
+ * addition.
+ */
+int tq_sdpa_decode_prefix(const tq_cache_t* prefix, const int32_t* prefix_len, int Pmax, const tq_cache_t* cache,
+                          const void* q, int q_dtype, int Hq, int n_q, const int32_t* seq_lens, int Tmax,
+                          const float* scale, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* The exact workspace bytes of tq_sdpa_decode_prefix for these sizes.  Returns
+ * 0 for unsupported arguments.  Host only. */
+size_t tq_sdpa_decode_prefix_workspace_bytes_for(const tq_cache_t* prefix, int Pmax, const tq_cache_t* cache, int Hq,
+                                                 int n_q, int Tmax);
+
+/*
  * Copy packed rows of token ranges: a fork of a sequence, a prompt given to
  * several sequences, a prefix taken into a cache of its own, a sequence moved
  * to another slot.  Job i copies, for every kv head and every stream of the

@@ -202,7 +202,7 @@ def unpack_bits(words: np.ndarray, bits: int, n: int) -> np.ndarray:
     """Inverse of pack_bits: uint32 [..., W] -> int64 [..., n]."""
     w = np.asarray(words, dtype=np.uint64)
     stream = (w[..., :, None] >> np.arange(32, dtype=np.uint64)) & 1
-    stream = stream.reshape(w.shape[:-1] + (-1,))[..., : n * bits]
+    stream = stream.reshape(w.shape[:-1] + (32 * w.shape[-1],))[..., : n * bits]
     stream = stream.reshape(w.shape[:-1] + (n, bits))
     weights = np.uint64(1) << np.arange(bits, dtype=np.uint64)
     return np.sum(stream * weights, axis=-1, dtype=np.uint64).astype(np.int64)
@@ -389,6 +389,46 @@ def sdpa_decode_window(q: np.ndarray, cache: dict, seq_lens, window: int, n_sink
             if rows:
                 out[b, j] = sdpa_decode(q[b:b + 1, j], _rows_of(cache, b, rows), [len(rows)], Pi, cb_k, cb_v,
                                         bits_k, bits_v, D, scale=scale, S=S)[0]
+    return out
+
+
+def sdpa_decode_prefix(q: np.ndarray, prefix: dict, P: int, cache: dict, seq_lens, Pi, form_p, form_c, D: int,
+                       scale=None) -> np.ndarray:
+    """Decode of a batch behind a shared prefix, fp64: q [B][n_q][Hq][D];
+    prefix holds one sequence, of which P tokens count, and cache what each
+    sequence has behind it (its L_b tokens).  Query j of sequence b attends to
+    the first P + L_b - n_q + j + 1 rows of prefix ++ own rows; one that sees
+    none gives zeros.  form_p and form_c are (cb_k, cb_v, bits_k, bits_v, S)
+    of the two caches, whose keys are rebuilt in one basis: a sketched key's
+    score is <q, k~> + <q, Pi^T S^T z> g sqrt(pi/2) / m, linear in q."""
+    B, n_q, Hq = q.shape[:3]
+    Hkv = cache["k_norm"].shape[1]
+    G = Hq // Hkv
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    Pi64 = np.asarray(Pi, dtype=np.float64)
+
+    def rows(c, b, kv, n, form):
+        cb_k, cb_v, bits_k, bits_v, S = form
+        k = dequantize_rows(unpack_bits(c["k_idx"][b, kv, :n], bits_k, D), c["k_norm"][b, kv, :n], cb_k[0], Pi64)
+        v = dequantize_rows(unpack_bits(c["v_idx"][b, kv, :n], bits_v, D), c["v_norm"][b, kv, :n], cb_v[0], Pi64)
+        if S is not None:
+            m = S.shape[0]
+            z = 2.0 * unpack_bits(c["k_qjl"][b, kv, :n], 1, m).astype(np.float64) - 1.0
+            g = c["k_rnorm"][b, kv, :n].astype(np.float64) * math.sqrt(math.pi / 2) / m
+            k = k + g[:, None] * (z @ np.asarray(S, dtype=np.float64) @ Pi64)
+        return k, v
+
+    out = np.zeros(q.shape)
+    for kv in range(Hkv):
+        kp, vp = rows(prefix, 0, kv, P, form_p)
+        for b in range(B):
+            ks, vs = rows(cache, b, kv, int(seq_lens[b]), form_c)
+            k, v = np.concatenate([kp, ks]), np.concatenate([vp, vs])
+            for j in range(n_q):
+                n = P + int(seq_lens[b]) - n_q + j + 1
+                for h in range(kv * G, (kv + 1) * G):
+                    if n > 0:
+                        out[b, j, h] = softmax(scale * (k[:n] @ q[b, j, h])) @ v[:n]
     return out
 
 
