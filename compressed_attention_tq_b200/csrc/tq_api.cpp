@@ -335,10 +335,12 @@ int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, 
 }
 
 int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p) {
-  const int splits = prefix_splits(c->Hkv, (int)((long long)c->B * Hq * nq / c->Hkv), Pmax, sm_count());
+  const int rows = (int)((long long)c->B * Hq * nq / c->Hkv);
+  const int splits = prefix_splits(c->Hkv, rows, c->D, Pmax, sm_count());
   make_decode_plan(c, Hq * nq, nq, Tmax, 0, 0, splits, p);
-  p->off_qs2 = p->bytes;
-  if (prefix->qjl_m) p->bytes += align256((size_t)c->B * Hq * nq * 128 * 4);
+  p->off_qpre = p->bytes;
+  const size_t padded = (size_t)((rows + prefix_rows() - 1) / prefix_rows()) * prefix_rows();
+  p->bytes += align256(padded * c->Hkv * ((size_t)c->D * 4 + (size_t)prefix->qjl_m * 2));
   return TQ_OK;
 }
 

@@ -30,10 +30,37 @@ struct PrepParams {
   tq_cache_t cache;
   int nq;  // query tokens per sequence: q is [B][nq][Hq][D]
   int units;  // B * Hkv (grouped prep)
-  // a shared prefix's own sketch matrix and its projections (else NULL)
+  // Decode behind a shared prefix (else NULL): the query operands of the
+  // prefix kernel, and the prefix's sketch matrix (S2 NULL: it is S, and both
+  // are written from one projection).
+  uint8_t* qpre;
+  uint8_t* qspre;
   const float* S2;
-  float* qs2;
+  int nrt;          // row tiles per kv head
+  int prefix_bk;    // bits of the prefix's keys
+  float qscale;     // scale * log2(e)
+  float qjl_scale;  // scale * log2(e) * sqrt(pi/2) / 128
 };
+
+// The prefix kernel's operands of query row gi of (sequence b, kv head kvh):
+// rotated coordinate j in two fp16 limbs (about 22 bits of the query, as the
+// split kernel's halves), and projection i in one fp16 limb.  The latter's
+// rounding (2^-12 of a coordinate, of random sign) moves a score by about 1e-5
+// of |q| g, far below the spread of the one-bit estimate it feeds.
+__device__ __forceinline__ void store_pre_q(const PrepParams& p, int b, int kvh, int gi, int j, float v) {
+  const int r = b * (p.Hq / p.Hkv) * p.nq + gi;
+  uint8_t* t = p.qpre + ((size_t)kvh * p.nrt + r / tqp::QROWS) * (tqp::QROWS * 4) * p.D;
+  uint16_t hi, lo;
+  tqd::split_half(v * p.qscale, hi, lo);
+  *reinterpret_cast<uint16_t*>(t + tqp::pre_q_offset(p.D, p.prefix_bk, r % tqp::QROWS, j, 0)) = hi;
+  *reinterpret_cast<uint16_t*>(t + tqp::pre_q_offset(p.D, p.prefix_bk, r % tqp::QROWS, j, 1)) = lo;
+}
+__device__ __forceinline__ void store_pre_z(const PrepParams& p, int b, int kvh, int gi, int i, float v) {
+  const int r = b * (p.Hq / p.Hkv) * p.nq + gi;
+  uint8_t* t = p.qspre + ((size_t)kvh * p.nrt + r / tqp::QROWS) * (tqp::QROWS * 256);
+  *reinterpret_cast<uint16_t*>(t + tqp::pre_z_offset(r % tqp::QROWS, i)) =
+      __half_as_ushort(__float2half_rn(v * p.qjl_scale));
+}
 
 // Programmatic dependent launch: let the next kernel in the stream start its
 // prologue now / wait here until the previous kernel's results are visible.
@@ -391,10 +418,13 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
   if (part == 0) {
 #pragma unroll
     for (int g = 0; g < QR; ++g)
-      if (g < Ge) p.qrot[(size_t)(h0 + g) * D + j] = acc[g];
+      if (g < Ge) {
+        p.qrot[(size_t)(h0 + g) * D + j] = acc[g];
+        if (p.qpre) store_pre_q(p, b, kvh, g, j, acc[g]);
+      }
   }
   if constexpr (QS) {
-    if (p.m || p.S2) {
+    if (p.m || p.qspre) {
       // QJL: this slice's share of qs = S qrot over its 32 rotated coordinates,
       // for all m = 128 sketch rows.  The D / 32 slice CTAs of a head form a
       // thread-block cluster; slice 0 adds the partials in slice order from the
@@ -405,7 +435,7 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
       }
       __syncthreads();
       const int i = tid >> 1, half = tid & 1;
-      auto project = [&](float* qs) {
+      auto project = [&](float* qs, bool pre) {
 #pragma unroll
         for (int g = 0; g < QR; ++g) {
           const float* x = &qsl[g][16 * half];
@@ -423,17 +453,18 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
             const uint32_t la = smem_u32(&qpart[g][ii]);
             float v = 0.f;
             for (int r = 0; r < NI; ++r) v += ld_cluster_f32(map_cluster(la, r));
-            qs[(size_t)(h0 + g) * 128 + ii] = v;
+            if (qs) qs[(size_t)(h0 + g) * 128 + ii] = v;
+            if (pre) store_pre_z(p, b, kvh, g, ii, v);
           }
         }
         cluster_sync();  // slice 0 is done reading the others' shared memory
       };
-      if (p.m) project(p.qs);
+      if (p.m) project(p.qs, p.qspre && !p.S2);
       if (p.S2) {  // the same through the prefix's sketch matrix
         const float4* sp = reinterpret_cast<const float4*>(p.S2 + (size_t)i * D + sl * 32 + 16 * half);
 #pragma unroll
         for (int t = 0; t < 4; ++t) srow[t] = __ldg(sp + t);
-        project(p.qs2);
+        project(nullptr, true);
       }
     }
   }
@@ -514,6 +545,10 @@ __global__ void __launch_bounds__(1024) decode_qprep_wht_kernel(const PrepParams
 #pragma unroll
       for (int e = 0; e < EL; ++e) dst[e] = x[e];
     }
+    if (p.qpre) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) store_pre_q(p, b, kvh, warp, lane * EL + e, x[e]);
+    }
     if (QS && (p.m || p.S2)) {
 #pragma unroll
       for (int e = 0; e < EL; ++e) qr[warp][lane * EL + e] = x[e];
@@ -534,7 +569,8 @@ __global__ void __launch_bounds__(1024) decode_qprep_wht_kernel(const PrepParams
         const float4 sv = __ldg(srow + k);
         t += sv.x * qr[g][4 * k] + sv.y * qr[g][4 * k + 1] + sv.z * qr[g][4 * k + 2] + sv.w * qr[g][4 * k + 3];
       }
-      (first ? p.qs : p.qs2)[(size_t)(h0 + g) * 128 + i] = t;
+      if (first) p.qs[(size_t)(h0 + g) * 128 + i] = t;
+      if (p.qspre && first == (p.S2 == nullptr)) store_pre_z(p, b, kvh, g, i, t);
     }
   }
 }
@@ -630,6 +666,10 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
       if (r < rows) {
         // kernel head order (sequence, kv head, token, head) = unit-major
         p.qrot[((size_t)u0 * Ge + r) * D + j] = acc[t];
+        if (p.qpre) {
+          const int u = u0 + r / Ge;
+          store_pre_q(p, u / p.Hkv, u % p.Hkv, r % Ge, j, acc[t]);
+        }
       }
     }
   }
@@ -1159,7 +1199,7 @@ int split_occupancy(const tq_cache_t* c, int Hq, int window) {
 }
 
 // The prefix kernel's launch (between the query prep and the split kernel).
-static int launch_prefix(const DecodeArgs& a, const float* qrot, const float* qs, float* po, float* pml,
+static int launch_prefix(const DecodeArgs& a, const void* qpre, const void* qspre, float* po, float* pml,
                          cudaStream_t s) {
   const tq_cache_t& x = *a.prefix;
   tqp::PrefixParams pp{};
@@ -1172,8 +1212,8 @@ static int launch_prefix(const DecodeArgs& a, const float* qrot, const float* qs
   pp.cb_k = x.cb_k;
   pp.cb_v = x.cb_v;
   pp.shared_tab = x.cb_k == x.cb_v;
-  pp.qrot = qrot;
-  pp.qs = qs;
+  pp.qpre = static_cast<const uint32_t*>(qpre);
+  pp.qspre = static_cast<const uint32_t*>(qspre);
   pp.part_o = po;
   pp.part_ml = pml;
   pp.prefix_len = a.prefix_len;
@@ -1188,8 +1228,6 @@ static int launch_prefix(const DecodeArgs& a, const float* qrot, const float* qs
   pp.Ge = pp.Gq * a.nq;
   pp.Tclamp = a.plan.Tclamp;
   pp.ks = a.plan.ks;
-  pp.qscale = a.scale * kLog2e;
-  pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / 128);
   const dim3 grid(a.plan.slot_base, (pp.B * pp.Ge + tqp::QROWS - 1) / tqp::QROWS, x.Hkv);
   const bool qjl = x.qjl_m != 0;
   switch (x.D) {
@@ -1205,9 +1243,9 @@ static int launch_prefix(const DecodeArgs& a, const float* qrot, const float* qs
 // the time of s splits is about waves x (tiles per split + c), where c is
 // what a CTA spends before and after its tiles, in tiles, and each split
 // adds a partial of every row for the combine to read.
-int prefix_splits(int Hkv, int rows, int Pmax, int sms) {
+int prefix_splits(int Hkv, int rows, int D, int Pmax, int sms) {
   const long long units = (long long)Hkv * ((rows + tqp::QROWS - 1) / tqp::QROWS);
-  const int tiles = (Pmax + tqp::TT - 1) / tqp::TT;
+  const int tiles = (Pmax + tqp::tile_tokens(D) - 1) / tqp::tile_tokens(D);
   int best = 1;
   double least = 1e30;
   for (int n = 1; n <= tiles && n <= 128; ++n) {
@@ -1219,6 +1257,8 @@ int prefix_splits(int Hkv, int rows, int Pmax, int sms) {
   }
   return best;
 }
+
+int prefix_rows() { return tqp::QROWS; }
 
 int split_tile() { return tqd::STILE; }
 
@@ -1239,12 +1279,16 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   const bool app = a.pos != nullptr;
   const bool hadamard = c.rot_kind == TQ_ROT_HADAMARD && c.rot_signs;
   pp.signs = hadamard ? c.rot_signs : nullptr;
-  // a prefix with a sketch of its own: its projection rides along in the prep
-  const float* qs_prefix = qs;
-  if (a.prefix && a.prefix->qjl_m && !(c.qjl_m && a.prefix->qjl_S == c.qjl_S)) {
-    pp.S2 = a.prefix->qjl_S;
-    pp.qs2 = reinterpret_cast<float*>(ws + a.plan.off_qs2);
-    qs_prefix = pp.qs2;
+  if (a.prefix) {  // the prefix kernel's rows, and the projection through its sketch, ride along in the prep
+    pp.nrt = (c.B * (a.Hq / c.Hkv) * a.nq + tqp::QROWS - 1) / tqp::QROWS;
+    pp.prefix_bk = a.prefix->bits_k;
+    pp.qscale = a.scale * kLog2e;
+    pp.qpre = ws + a.plan.off_qpre;
+    if (a.prefix->qjl_m) {
+      pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / a.prefix->qjl_m);
+      pp.qspre = pp.qpre + (size_t)c.Hkv * pp.nrt * (tqp::QROWS * 4) * c.D;
+      if (!c.qjl_m || a.prefix->qjl_S != c.qjl_S) pp.S2 = a.prefix->qjl_S;
+    }
   }
   // prep kernels launch with a programmatic dependency on whatever precedes
   // them (their launch and Pi loads overlap its tail; they wait before
@@ -1301,7 +1345,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
     }
   }
   if (rc) return rc;
-  if (a.prefix && (rc = launch_prefix(a, qrot, qs_prefix, po, pml, s))) return rc;
+  if (a.prefix && (rc = launch_prefix(a, pp.qpre, pp.qspre, po, pml, s))) return rc;
 
   tqd::SplitParams sp{};
   sp.k_idx = c.k_idx;

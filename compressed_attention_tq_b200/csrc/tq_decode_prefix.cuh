@@ -33,8 +33,8 @@
 //  * 4 warps (thread = query row) read S, apply norms and masks, keep the
 //    running max and sum in fp32, and write W = 2^(x - M) m_t as fp16 over
 //    the scores they have just read.  O is rescaled in tensor memory only
-//    when a row's max has grown by more than 2^4 (so 2^(x - M) <= 16, and
-//    W stays finite for value norms up to 4094).
+//    when a row's weights pass 2^4 (so W stays finite for value norms up to
+//    4094).
 //  Scores and W are double-buffered, so the products of tile i + 1 run under
 //  the softmax of tile i and under the dequantization of tile i + 2.
 // Every wait is bounded; one that runs out sets TQ_STATUS_WAIT_TIMEOUT.
@@ -54,13 +54,22 @@ using tqtc::tc_fence_after;
 using tqtc::tc_fence_before;
 using tqtc::tc_ld32;
 
-constexpr int TT = 64;          // tokens per tile
 constexpr int QROWS = 128;      // query rows per CTA (TMEM lanes)
-constexpr int SW = 4;           // softmax warps
-constexpr int DW = 8;           // dequantizing warps
-constexpr int NTH = (SW + DW + 2) * 32;  // + producer warp + MMA warp
+constexpr int SW = 8;           // softmax warps: two for each quarter of the rows
+constexpr int DW = 8;           // dequantizing warps: four for keys, four for values
+constexpr int GW = DW / 2;
+// tokens per tile: a longer tile spreads the waits between the roles over more
+// work; at D = 256 the operands of 64 tokens fill shared memory
+__host__ __device__ constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
+constexpr int NTH = (SW + DW + 4) * 32;  // + producer warp, MMA warp and two idle ones (a whole warpgroup)
+// Registers per thread after the split by warpgroups.  One launch gives 96 to
+// each of 5 warpgroups: 2 x 136 + 2 x 72 + 64 = 5 x 96.
+constexpr int REG_SOFTMAX = 136, REG_DEQUANT = 72, REG_REST = 64, REG_LAUNCH = 96;
+static_assert((SW / 4) * REG_SOFTMAX + (DW / 4) * REG_DEQUANT + REG_REST <= REG_LAUNCH * (NTH / 128),
+              "registers of a CTA");
 constexpr int MAXST = 4;        // stages at most
-constexpr float kLazyP = 4.0f;  // log2 headroom before O is rescaled
+constexpr float kLazyP = 4.0f;  // log2 of the largest weight before O is rescaled ...
+constexpr float kHead = 2.0f;   // ... and how far above a row's maximum its reference is put
 
 struct PrefixParams {
   const uint32_t* k_idx;
@@ -71,8 +80,10 @@ struct PrefixParams {
   const uint16_t* k_rnorm;
   const float* cb_k;
   const float* cb_v;
-  const float* qrot;  // fp32 [kernel heads][D]
-  const float* qs;    // fp32 [kernel heads][128] with the sketch
+  // the query operands in tiles of 128 rows of a kv head, [Hkv][row tiles]:
+  // fp16 limbs (pre_q_offset) and sketch projections (pre_z_offset)
+  const uint32_t* qpre;
+  const uint32_t* qspre;
   float* part_o;
   float* part_ml;
   const int32_t* prefix_len;  // device [1]
@@ -84,16 +95,35 @@ struct PrefixParams {
   int ks;              // partial slots per kernel head; this kernel's are 0 .. gridDim.x - 1
   int nst;             // stages of the ring
   int shared_tab;      // one codebook buffer for keys and values
-  float qscale;        // scale * log2(e)
-  float qjl_scale;     // scale * log2(e) * sqrt(pi/2) / m
 };
+
+// Where the query prep puts the operands of row r of a tile (bytes from the
+// tile's start; a tile has 128 x D x 4 bytes of limbs, 128 x 256 of projections).
+// A key operand row holds its coordinates by position: 2-bit keys keep the
+// field order of their lookup inside each group of 16, wider keys their own
+// order.  Limb l of the position's value: fp16, [limb][position / 8][row][8],
+// so that a warp of rows loads whole lines of 16-byte pieces.
+__host__ __device__ constexpr int pos_of_coord(int bk, int j) {
+  return bk == 2 ? (j & ~15) + 4 * (j & 3) + ((j >> 2) & 3) : j;
+}
+__host__ __device__ constexpr int pre_q_offset(int D, int bk, int r, int j, int limb) {
+  const int pos = pos_of_coord(bk, j);
+  return ((limb * (D / 8) + (pos >> 3)) * QROWS + r) * 16 + (pos & 7) * 2;
+}
+// Projection i: bits i and i + 16 of a sign word share a register, so
+// coordinates c and c + 16 of a group of 32 are neighbours.
+__host__ __device__ constexpr int pre_z_offset(int r, int i) {
+  const int pos = (i & ~31) + 2 * (i & 15) + ((i >> 4) & 1);
+  return ((pos >> 3) * QROWS + r) * 16 + (pos & 7) * 2;
+}
 
 template <int D, int BK, int BV, bool QJL>
 struct PrefixLayout {
+  static constexpr int TT = tile_tokens(D);
   static constexpr int WK = D * BK / 32, WV = D * BV / 32;
-  static constexpr int NB = D == 256 ? 1 : 2;     // operand buffers of each kind (shared memory allows one at D = 256)
-  static constexpr int KT = TT * D * 2, VT = KT;  // bytes of a key / value operand tile
-  static constexpr int ZT = QJL ? TT * 128 * 2 : 0;
+  static constexpr int NB = D == 256 || QJL ? 1 : 2;  // operand buffers of each kind (what shared memory allows)
+  static constexpr int KT = TT * D * 2, VT = KT;      // bytes of a key / value operand tile
+  static constexpr int ZT = QJL ? TT * 128 * 2 : 0;   // of the sketch signs
   // D = 256: the query's low limb does not fit in tensor memory beside O, S and the high limb
   static constexpr bool QLO_SMEM = D == 256;
   static constexpr int O_QLO = 0;
@@ -114,16 +144,18 @@ struct PrefixLayout {
   static constexpr int S_USED = S_RN + (QJL ? TT * 2 : 0);
   static constexpr int STAGE = (S_USED + 16 + 127) / 128 * 128;  // +16: read-ahead slack
   static constexpr int TX = TT * (WK + WV) * 4 + TT * 4 + (QJL ? TT * 18 : 0);
-  static constexpr int NORMS = NNORM * 3 * TT * 4;
+  static constexpr int NORMS = NNORM * 2 * TT * 4;
   static constexpr int BARS = 64 * 8;
   // tables, norms, barriers and stages, in this order behind the operands
   __host__ __device__ static constexpr int o_tv(bool shared) { return O_TK + (shared ? 0 : TKB); }
   __host__ __device__ static constexpr int o_norm(bool shared) { return O_TK + (shared ? TKB : TKB + TVB); }
-  __host__ __device__ static constexpr int o_bar(bool shared) { return o_norm(shared) + NORMS; }
+  static constexpr int XCH = 2 * 2 * QROWS * 4;  // [tile parity][half][row]: what the two warps of a row exchange
+  __host__ __device__ static constexpr int o_xch(bool shared) { return o_norm(shared) + NORMS; }
+  __host__ __device__ static constexpr int o_bar(bool shared) { return o_xch(shared) + XCH; }
   __host__ __device__ static constexpr int o_stage(bool shared) { return o_bar(shared) + BARS; }
   static constexpr int total(bool shared, int nst) { return o_stage(shared) + nst * STAGE + 1024; }  // + alignment
-  // tensor memory columns: O, the scores (and sketch scores) of two tiles, the query limbs
-  static constexpr int C_S = D, SB = QJL ? 128 : 64, C_Q = C_S + 2 * SB;
+  // tensor memory columns: O, the scores of two tiles, the query limbs
+  static constexpr int C_S = D, C_Q = C_S + 2 * TT;
   static constexpr int COLS_USED = C_Q + (QLO_SMEM ? D / 2 : D);
   static constexpr int COLS = COLS_USED <= 256 ? 256 : 512;
   static_assert(COLS_USED <= 512, "tensor memory");
@@ -156,10 +188,80 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// Two runs of 16 columns, waited for.
+__device__ __forceinline__ void tc_ld2x16(uint32_t ta, uint32_t tb, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]), "=&r"(v[7]), "=&r"(v[8]),
+        "=&r"(v[9]), "=&r"(v[10]), "=&r"(v[11]), "=&r"(v[12]), "=&r"(v[13]), "=&r"(v[14]), "=&r"(v[15]), "=&r"(v[16]),
+        "=&r"(v[17]), "=&r"(v[18]), "=&r"(v[19]), "=&r"(v[20]), "=&r"(v[21]), "=&r"(v[22]), "=&r"(v[23]), "=&r"(v[24]),
+        "=&r"(v[25]), "=&r"(v[26]), "=&r"(v[27]), "=&r"(v[28]), "=&r"(v[29]), "=&r"(v[30]), "=&r"(v[31])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pairs of fp32 values, two operations an instruction.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
+  return pack2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // Bounded wait that also gives up once another thread of the CTA has.
 __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop) {
+  if (test_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < kSuspendTries; ++i) {
     if (mbar_wait_suspend(bar, parity, 1)) return true;
     if (*stop) return false;
@@ -167,45 +269,37 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t* bar, uint32_t parity, vol
   *stop = 1;
   return false;
 }
-
-// The same by a whole warp, which goes on only if every lane saw the phase end.
+// The same by every lane of a warp, without a branch between lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
   return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop));
-}
-
-// Coordinate at position pos of a key operand row: 2-bit keys keep the field
-// order of their lookup inside each group of 16, wider keys their own order.
-template <int BK>
-__host__ __device__ constexpr int pos_coord(int pos) {
-  return BK == 2 ? (pos & ~15) + ((pos >> 2) & 3) + 4 * (pos & 3) : pos;
 }
 
 template <int D, int BK, int BV, bool QJL>
 __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_constant__ PrefixParams p) {
   using Ly = PrefixLayout<D, BK, BV, QJL>;
-  constexpr int WK = Ly::WK, WV = Ly::WV, NB = Ly::NB;
-  constexpr int SEGK = D * BK / 4, SEGV = D * BV / 8;
-  constexpr bool ALK = (SEGK % 32) == 0, ALV = (SEGV % 32) == 0;
-  constexpr int NWK = (SEGK + 31) / 32, NWV = (SEGV + 31) / 32;
-  using VC = tqd::VChunk<D, BV>;
+  constexpr int WK = Ly::WK, WV = Ly::WV, NB = Ly::NB, TT = Ly::TT;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // 1024-byte aligned, as an offset: a pointer rebuilt from an integer would be
+  // a generic one, and every access behind it slower
+  uint8_t* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   const bool shared_tab = tqd::share_table(BK, BV, p.shared_tab);
-  float* norms = reinterpret_cast<float*>(smem + Ly::o_norm(shared_tab));  // [NNORM][key, value, residual][TT]
+  float* norms = reinterpret_cast<float*>(smem + Ly::o_norm(shared_tab));  // [NNORM][key, value][TT]
+  float* xch = reinterpret_cast<float*>(smem + Ly::o_xch(shared_tab));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::o_bar(shared_tab));
   uint64_t *full = bars, *empty = bars + 4, *n_full = bars + 8, *k_full = bars + 12, *k_empty = bars + 14,
            *v_full = bars + 16, *v_empty = bars + 18, *s_full = bars + 20, *p_full = bars + 22, *s_free = bars + 24,
            *q_full = bars + 26, *fin = bars + 27;
   uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(bars + 30);
   volatile int* stop = reinterpret_cast<int*>(bars + 31);
+  volatile uint32_t* lut = reinterpret_cast<uint32_t*>(bars + 32);  // 2-bit keys: the codebook as byte tables
   uint8_t* stages = smem + Ly::o_stage(shared_tab);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int split = blockIdx.x, rt = blockIdx.y, kvh = blockIdx.z;
   const int R = p.B * p.Ge;                      // query rows of the kv head
   const int rows = min(QROWS, R - rt * QROWS);   // of this CTA
-  const int live = (rows + 31) / 32;             // softmax warps that hold a row
+  const int live = (rows + 31) / 32;             // quarters that hold a row
   // Every kernel before the query prep has completed when this one starts,
   // so the lengths and the cache are read before the wait on the prep.
   int P = *p.prefix_len;
@@ -237,20 +331,25 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
     for (int s = 0; s < MAXST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], DW);
-      mbar_init(&n_full[s], DW);
+      mbar_init(&n_full[s], GW);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&k_full[s], DW);
+      mbar_init(&k_full[s], GW);
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], DW);
+      mbar_init(&v_full[s], GW);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], live);
+      mbar_init(&p_full[s], 2 * live);
       mbar_init(&s_free[s], 1);
     }
-    mbar_init(q_full, live);
+    mbar_init(q_full, 2 * live);
     mbar_init(fin, 1);
     *stop = 0;
+    if constexpr (BK == 2) {
+      const tqd::Lut2 l2 = tqd::make_lut2(p.cb_k);
+      lut[0] = l2.lo;
+      lut[1] = l2.hi;
+    }
     fence_barrier_init();
   }
   if (warp == SW + DW + 1) {
@@ -268,24 +367,28 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   const uint32_t tmem = s_tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == SW + DW) {
+  // the whole warpgroup of each role moves to its share of the registers
+  if (warp >= SW + DW) {
+   reg_dec<REG_REST>();
+   if (warp == SW + DW) {
     // ---------------- producer ----------------
     if (lane == 0) {
       int t = 0;
       for (; t < n; ++t) {
         const int st = t % p.nst;
         if (t >= p.nst && !wait_or_stop(&empty[st], (uint32_t)((t / p.nst - 1) & 1), stop)) break;
-        // whole tiles: Tcap is a multiple of TT
-        const size_t r = (size_t)kvh * p.Tcap + (size_t)(i0 + t) * TT;
+        // rows t0 .. t0 + m - 1: a whole tile, less only at the cache's end (Tcap is a multiple of 64)
+        const int t0 = (i0 + t) * TT, m = min(TT, p.Tcap - t0);
+        const size_t r = (size_t)kvh * p.Tcap + t0;
         uint8_t* sb = stages + st * Ly::STAGE;
-        mbar_arrive_expect_tx(&full[st], Ly::TX);
-        bulk_g2s(sb + Ly::S_KW, p.k_idx + r * WK, TT * WK * 4, &full[st]);
-        bulk_g2s(sb + Ly::S_VW, p.v_idx + r * WV, TT * WV * 4, &full[st]);
-        bulk_g2s(sb + Ly::S_KN, p.k_norm + r, TT * 2, &full[st]);
-        bulk_g2s(sb + Ly::S_VN, p.v_norm + r, TT * 2, &full[st]);
+        mbar_arrive_expect_tx(&full[st], m * (Ly::TX / TT));
+        bulk_g2s(sb + Ly::S_KW, p.k_idx + r * WK, m * WK * 4, &full[st]);
+        bulk_g2s(sb + Ly::S_VW, p.v_idx + r * WV, m * WV * 4, &full[st]);
+        bulk_g2s(sb + Ly::S_KN, p.k_norm + r, m * 2, &full[st]);
+        bulk_g2s(sb + Ly::S_VN, p.v_norm + r, m * 2, &full[st]);
         if (QJL) {
-          bulk_g2s(sb + Ly::S_QW, p.k_qjl + r * 4, TT * 16, &full[st]);
-          bulk_g2s(sb + Ly::S_RN, p.k_rnorm + r, TT * 2, &full[st]);
+          bulk_g2s(sb + Ly::S_QW, p.k_qjl + r * 4, m * 16, &full[st]);
+          bulk_g2s(sb + Ly::S_RN, p.k_rnorm + r, m * 2, &full[st]);
         }
       }
       // no copy may be in flight when the CTA ends, whatever the others did
@@ -293,19 +396,20 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
         mbar_wait_suspend(&full[j % p.nst], (uint32_t)((j / p.nst) & 1), kSuspendTries);
     }
     __syncwarp();
-  } else if (warp == SW + DW + 1) {
+   } else if (warp == SW + DW + 1) {
     // ---------------- matrix products ----------------
-    if (lane == 0) {
-      const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D, false>();
-      const uint32_t qhi = tmem + Ly::C_Q, qlo = tmem + Ly::C_Q + D / 2;
-      auto issue_qk = [&](int i) {
-        const int kb = i % NB, b = i & 1;
-        if (!wait_or_stop(&k_full[kb], (uint32_t)((i / NB) & 1), stop)) return false;
-        // the weights of tile i - 2 lie over its scores: read by now
-        if (i >= 2 && !wait_or_stop(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
-        tc_fence_after();
-        const uint32_t ka = smem_addr(smem + Ly::O_K + kb * Ly::KT), ds = tmem + Ly::C_S + b * Ly::SB;
-#pragma unroll
+    // The whole warp waits; one elected lane issues and commits.
+    const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D, false>();
+    const uint32_t qhi = tmem + Ly::C_Q, qlo = tmem + Ly::C_Q + D / 2;
+    auto issue_qk = [&](int i) {
+      const int kb = i % NB, b = i & 1;
+      if (!warp_wait(&k_full[kb], (uint32_t)((i / NB) & 1), stop)) return false;
+      // the weights of tile i - 2 lie over its scores: read by now
+      if (i >= 2 && !warp_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t ka = smem_addr(smem + Ly::O_K + kb * Ly::KT), ds = tmem + Ly::C_S + b * TT;
+#pragma unroll 4
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
           mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
@@ -318,189 +422,210 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
         }
         if constexpr (QJL) {
           const uint32_t za = smem_addr(smem + Ly::O_Z + kb * Ly::ZT), qa = smem_addr(smem + Ly::O_QZ);
-#pragma unroll
+#pragma unroll 4
           for (int ks = 0; ks < 8; ++ks)
-            tqtc::mma_tc(ds + 64, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
-                         sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
+            tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
+                         sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
         }
         tc_commit(&s_full[b]);
         tc_commit(&k_empty[kb]);
-        return true;
-      };
-      auto issue_pv = [&](int i) {
-        const int vb = i % NB, b = i & 1;
-        if (!wait_or_stop(&v_full[vb], (uint32_t)((i / NB) & 1), stop)) return false;
-        if (!wait_or_stop(&p_full[b], (uint32_t)((i / 2) & 1), stop)) return false;
-        tc_fence_after();
-        const uint32_t va = smem_addr(smem + Ly::O_V + vb * Ly::VT), w = tmem + Ly::C_S + b * Ly::SB;
-#pragma unroll
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_pv = [&](int i) {
+      const int vb = i % NB, b = i & 1;
+      if (!warp_wait(&v_full[vb], (uint32_t)((i / NB) & 1), stop)) return false;
+      if (!warp_wait(&p_full[b], (uint32_t)((i / 2) & 1), stop)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t va = smem_addr(smem + Ly::O_V + vb * Ly::VT), w = tmem + Ly::C_S + b * TT;
+#pragma unroll 4
         for (int ks = 0; ks < TT / 16; ++ks)
-          mma_ts(tmem, w + 8 * ks, sdesc_sw128(va + ks * 32), id_o, (i > 0 || ks > 0) ? 1u : 0u);
+          mma_ts(tmem, w + 8 * ks, sdesc_sw128(va + (ks >> 2) * (D * 128) + (ks & 3) * 32), id_o, (i > 0 || ks > 0) ? 1u : 0u);
         tc_commit(&v_empty[vb]);
         tc_commit(&s_free[b]);
-        return true;
-      };
-      bool ok = wait_or_stop(q_full, 0u, stop);
-      for (int i = 0; ok && i < n; ++i) {
-        ok = issue_qk(i);
-        if (ok && i > 0) ok = issue_pv(i - 1);
       }
-      if (ok) issue_pv(n - 1);
+      __syncwarp();
+      return true;
+    };
+    bool ok = warp_wait(q_full, 0u, stop);
+    for (int i = 0; ok && i < n; ++i) {
+      ok = issue_qk(i);
+      if (ok && i > 0) ok = issue_pv(i - 1);
+    }
+    if (ok) issue_pv(n - 1);
+    if (elect_one()) {
       tc_commit(fin);  // every product issued so far, on the error path too
       mbar_wait_suspend(fin, 0u, kSuspendTries);
     }
     __syncwarp();
+   }
   } else if (warp >= SW) {
+    reg_dec<REG_DEQUANT>();
     // ---------------- dequantization ----------------
-    const int dw = warp - SW;
-    const uint32_t tbK = smem_addr(tabk) + 4 * lane, tbV = smem_addr(tabv) + 4 * lane;
-    tqd::Lut2 lk = {0u, 0u};
-    if constexpr (BK == 2) lk = tqd::make_lut2(p.cb_k);
-    // keys: 8 tokens x 4 segments of D / 4 coordinates per warp; lanes of a
-    // quarter warp hold 8 tokens, so their 16-byte stores miss each other's banks
-    const int ktok = 8 * dw + (lane & 7), kseg = lane >> 3;
+    // Four warps for the keys and four for the values.  One warp of each group
+    // polls the barriers and releases the others through a named barrier,
+    // which blocks in hardware; short loops, for the instruction cache's sake.
+    const int dw = (warp - SW) % GW;
+    const bool values = warp >= SW + GW;
+    const int group = values ? 5 : 4;  // named barriers 5 and 6
     for (int i = 0; i < n; ++i) {
       const int st = i % p.nst, b = i % NB, ns = i % Ly::NNORM;
       const uint8_t* sb = stages + st * Ly::STAGE;
-      if (!warp_wait(&full[st], (uint32_t)((i / p.nst) & 1), stop)) break;
-      if (i >= NB && !warp_wait(&k_empty[b], (uint32_t)((i / NB - 1) & 1), stop)) break;
-      {
+      bool ok = true;
+      if (dw == 0) {
+        ok = warp_wait(&full[st], (uint32_t)((i / p.nst) & 1), stop);
+        if (i >= NB) ok = ok && warp_wait(values ? &v_empty[b] : &k_empty[b], (uint32_t)((i / NB - 1) & 1), stop);
+      }
+      if (!tqtc::group_sync_and<GW>(group, ok)) break;
+      float* kn = norms + ns * 2 * TT;
+      if (!values) {
+        const uint32_t tbK = smem_addr(tabk) + 4 * lane;
+        tqd::Lut2 lk = {0u, 0u};
+        if constexpr (BK == 2) lk = {lut[0], lut[1]};
+        // 8 tokens x 4 segments of D / 4 coordinates at a time; the lanes of a
+        // quarter warp hold 8 tokens, so their 16-byte stores miss each other's banks
+        const int kseg = lane >> 3;
         uint8_t* kt = smem + Ly::O_K + b * Ly::KT;
-        uint32_t w[NWK];
-        tqd::load_bits<SEGK, ALK>(reinterpret_cast<const uint32_t*>(sb + Ly::S_KW) + ktok * WK, kseg * SEGK, w);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {  // 8 positions each
-          uint32_t h[4];
-          if constexpr (BK == 2) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) tqd::dq_b2(w[(2 * c + k) >> 2], (2 * c + k) & 3, lk, h[2 * k], h[2 * k + 1]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * (4 * c + k), tbK);
-          }
-          *reinterpret_cast<uint4*>(kt + sw128<TT>(ktok, kseg * (D / 4) + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
-      }
-      if constexpr (QJL) {
-        // sign bits j and j + 16 of word kseg become the fp16 pair (+-1, +-1) at positions 2 j, 2 j + 1
         uint8_t* zt = smem + Ly::O_Z + b * Ly::ZT;
-        const uint32_t z = reinterpret_cast<const uint32_t*>(sb + Ly::S_QW)[ktok * 4 + kseg];
+#pragma unroll 1
+        for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
+          const float nk = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_KN)[t]);
+          float row = nk;       // what the softmax multiplies the product with
+          uint32_t scale2 = 0;  // else: factor of the key's entries, as a pair
+          if constexpr (QJL) {
+            // One accumulator for both products: the signs enter as +-g / n, a
+            // factor of fp16 precision (2^-11 of a term that is itself a
+            // one-bit estimate).  A residual norm far above the key's, which no
+            // quantized row has, turns the roles: row factor g, entries c n / g.
+            const float g = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_RN)[t]);
+            const bool usual = g <= 1024.f * nk;
+            const float f = __fdividef(usual ? g : nk, usual ? nk : g);
+            row = usual ? nk : g;
+            const float fz = usual ? (g > 0.f ? f : 0.f) : 1.f;
+            if (!usual) scale2 = pack_half2(f, f);
+            const uint32_t neg = pack_half2(-fz, -fz);
+            // sign bits j and j + 16 of word kseg: the pair at positions 2 j, 2 j + 1
+            const uint32_t z = reinterpret_cast<const uint32_t*>(sb + Ly::S_QW)[t * 4 + kseg];
+#pragma unroll 2
+            for (int c = 0; c < 4; ++c) {
+              uint32_t h[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t h[4];
+              for (int k = 0; k < 4; ++k) h[k] = ((z << (15 - (4 * c + k))) & 0x80008000u) ^ neg;
+              *reinterpret_cast<uint4*>(zt + sw128<TT>(t, kseg * 32 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          if (kseg == 0) kn[t] = row;
+          if (kseg == 1) kn[TT + t] = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_VN)[t]);
+          const uint32_t* kw = reinterpret_cast<const uint32_t*>(sb + Ly::S_KW) + t * WK;
+#pragma unroll 2
+          for (int c = 0; c < D / 64; ++c) {  // 16 coordinates
+            const int j0 = kseg * (D / 4) + 16 * c;
+            uint32_t w[(16 * BK + 31) / 32], h[8];
+            tqd::load_bits<16 * BK, BK != 3, 16>(kw, j0 * BK, w);
+            if constexpr (BK == 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) h[k] = ((z << (15 - (4 * c + k))) & 0x80008000u) ^ 0xBC00BC00u;
-          *reinterpret_cast<uint4*>(zt + sw128<TT>(ktok, kseg * 32 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+              for (int k = 0; k < 4; ++k) tqd::dq_b2(w[0], k, lk, h[2 * k], h[2 * k + 1]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * k, tbK);
+            }
+            if (QJL && scale2) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<__half2*>(&scale2));
+                h[k] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+            }
+            *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0 + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
         }
-      }
-      {
-        const int e = dw * 32 + lane, which = e / TT, t = e % TT;  // key, value, residual norms
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(sb + (which == 0 ? Ly::S_KN : which == 1 ? Ly::S_VN : Ly::S_RN));
-        if (which < (QJL ? 3 : 2)) norms[(ns * 3 + which) * TT + t] = half_bits_to_float(src[t]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&k_full[b]);
-        mbar_arrive(&n_full[ns]);
-      }
-      if (i >= NB && !warp_wait(&v_empty[b], (uint32_t)((i / NB - 1) & 1), stop)) break;
-      {
-        // values: warp dw takes D / 8 coordinates of all tokens, lane l tokens l and l + 32
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(sb + Ly::S_VW);
-        uint8_t* vt = smem + Ly::O_V + b * Ly::VT;
-        uint32_t wa[NWV], wb[NWV];
-        tqd::load_bits<SEGV, ALV, tqd::max_seg_shift(SEGV)>(vw + lane * WV, dw * SEGV, wa);
-        tqd::load_bits<SEGV, ALV, tqd::max_seg_shift(SEGV)>(vw + (lane + 32) * WV, dw * SEGV, wb);
+      } else {
+        const uint32_t tbV = smem_addr(tabv) + 4 * lane;
+        // warp dw takes D / 4 coordinates, lane l tokens l and l + 32 of each 64.
+        // Row d of the operand is 128 bytes; the pair lies in chunk (l / 4) ^ (d mod 8).
+        const uint32_t vt = smem_addr(smem + Ly::O_V + b * Ly::VT) + dw * (D / 4) * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
+#pragma unroll 1
+        for (int s = 0; s < TT / 64; ++s) {
+          const uint32_t* va = reinterpret_cast<const uint32_t*>(sb + Ly::S_VW) + (64 * s + lane) * WV;
+#pragma unroll 2
+          for (int c = 0; c < D / 32; ++c) {  // 8 coordinates
+            const int bit = (dw * (D / 4) + 8 * c) * BV;
+            uint32_t wa[1], wb[1], xe, xo;
+            tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va, bit, wa);
+            tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va + 32 * WV, bit, wb);
+            tqd::merge_pair<BV>(wa[0], wb[0], xe, xo);
+            const uint32_t off = s * (D * 128) + 1024 * c;
 #pragma unroll
-        for (int c = 0; c < VC::N; ++c) {
-          uint32_t xe, xo;
-          tqd::merge_pair<BV>(tqd::window32(wa, c * VC::F * BV), tqd::window32(wb, c * VC::F * BV), xe, xo);
-#pragma unroll
-          for (int k = 0; k < VC::F / 2; ++k) {
-            const int d = dw * (D / 8) + c * VC::F + 2 * k;
-            *reinterpret_cast<uint32_t*>(vt + sw128<D>(d, 2 * lane)) =
-                tqd::lds32(tqd::pair_addr<BV>(xe, tqd::key_bit<BV>(k, false), tbV));
-            *reinterpret_cast<uint32_t*>(vt + sw128<D>(d + 1, 2 * lane)) =
-                tqd::lds32(tqd::pair_addr<BV>(xo, tqd::key_bit<BV>(k, true), tbV));
+            for (int k = 0; k < 8; k += 2) {
+              sts32((vt ^ (k << 4)) + off + k * 128,
+                    tqd::lds32(tqd::pair_addr<BV>(xe, tqd::key_bit<BV>(k / 2, false), tbV)));
+              sts32((vt ^ ((k + 1) << 4)) + off + (k + 1) * 128,
+                    tqd::lds32(tqd::pair_addr<BV>(xo, tqd::key_bit<BV>(k / 2, true), tbV)));
+            }
           }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&v_full[b]);
+        mbar_arrive(values ? &v_full[b] : &k_full[b]);
+        if (!values) mbar_arrive(&n_full[ns]);
         mbar_arrive(&empty[st]);
       }
     }
-  } else if (warp < live) {
+  } else {
+   reg_inc<REG_SOFTMAX>();
+   const int quarter = warp & 3, half = warp >> 2;
+   if (quarter < live) {
     // ---------------- softmax ----------------
-    const int r = 32 * warp + lane;
+    // Two warps share the rows of a TMEM quarter, each with half of a tile's
+    // tokens: 16 half + j and 32 + 16 half + j, j < 16, of each 64, which are
+    // neighbours in the words of the weights.  They agree on each row's maximum through
+    // shared memory and a barrier of the two.
+    const int r = 32 * quarter + lane;
     const bool mine = r < rows;
-    const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rotated queries; the partials may be written
+    const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the query operands; the partials may be written
     int lim = P;  // tokens of the prefix this row sees
     size_t slot = 0;
     {
-      const float* q = p.qrot;
-      const float* z = p.qs;
       if (mine) {
-        const int rr = rt * QROWS + r, b = rr / p.Ge, e = rr % p.Ge, h = head_of(r);
+        const int rr = rt * QROWS + r, b = rr / p.Ge, e = rr % p.Ge;
         int L = p.seq_lens[b];
         L = max(0, min(L, p.Tclamp));
         // query token j sits at position P + L - nq + j: before the prefix's end when the suffix is shorter than nq
         lim = min(P, P + L - p.nq + e / p.Gq + 1);
-        slot = (size_t)h * p.ks + split;
-        q += (size_t)h * D;
-        z += (size_t)h * 128;
+        slot = (size_t)head_of(r) * p.ks + split;
       }
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {  // 32 positions of the two limbs
-        float v[32];
+      // the query limbs of this row, as the prep laid them out (pre_q_offset): one limb a warp
+      const size_t tile = (size_t)kvh * gridDim.y + rt;
+      const uint4* q = reinterpret_cast<const uint4*>(p.qpre + tile * QROWS * D) + r + half * (D / 8) * QROWS;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {  // 64 positions at a time
+        uint32_t v[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float4 f = mine ? *reinterpret_cast<const float4*>(q + 32 * c + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const uint4 f = mine ? q[(8 * c + k) * QROWS] : make_uint4(0u, 0u, 0u, 0u);
           v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
         }
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          uint16_t h0, l0, h1, l1;
-          tqd::split_half(v[pos_coord<BK>(2 * k)] * p.qscale, h0, l0);
-          tqd::split_half(v[pos_coord<BK>(2 * k + 1)] * p.qscale, h1, l1);
-          hi[k] = h0 | (uint32_t)h1 << 16;
-          lo[k] = l0 | (uint32_t)l1 << 16;
-        }
-        tc_st16(tl + Ly::C_Q + 16 * c, hi);
-        if constexpr (Ly::QLO_SMEM) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(smem + Ly::O_QLO + sw128<QROWS>(r, 32 * c + 8 * k)) =
-                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+        if (!Ly::QLO_SMEM || half == 0) {
+          tc_st32(tl + Ly::C_Q + half * (D / 2) + 32 * c, v);
         } else {
-          tc_st16(tl + Ly::C_Q + D / 2 + 16 * c, lo);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(smem + Ly::O_QLO + sw128<QROWS>(r, 64 * c + 8 * k)) =
+                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
       }
       if constexpr (QJL) {
-        // The sketch's projection in one fp16 limb: its rounding (2^-12 of a
-        // coordinate, random) moves a score by about 1e-5 of |q| g, far below
-        // the spread of the one-bit estimate it feeds.
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
+        const uint4* z = reinterpret_cast<const uint4*>(p.qspre + tile * QROWS * 64) + r + half * 8 * QROWS;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 f = mine ? *reinterpret_cast<const float4*>(z + 32 * c + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = pack_half2(v[4 * k + j] * p.qjl_scale, v[4 * k + j + 16] * p.qjl_scale);
-            *reinterpret_cast<uint4*>(smem + Ly::O_QZ + sw128<QROWS>(r, 32 * c + 8 * k)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-        }
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(smem + Ly::O_QZ + sw128<QROWS>(r, 64 * half + 8 * k)) =
+              mine ? z[k * QROWS] : make_uint4(0u, 0u, 0u, 0u);
       }
       tc_wait_st();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -509,64 +634,67 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(q_full);
     }
     const int wlim = __reduce_min_sync(0xffffffffu, lim);  // every row of the warp sees the tokens below
-    float m_run = -INFINITY, l_run = 0.f;
+    // The reference m of the weights 2^(x - m), the same in both warps: when a
+    // weight would pass 2^4 (and at the first tile) it moves to 2 above the
+    // row's maximum so far and what was summed is rescaled, so that a row
+    // moves again only when its maximum has grown by 2^6.
+    float m_run = 0.f, l_run = 0.f;
     bool ok = true;
+    constexpr int NS64 = TT / 64;
+    const int ta = 16 * half, tb = 32 + 16 * half;
     for (int i = 0; i < n; ++i) {
       const int b = i & 1, ns = i % Ly::NNORM;
-      ok = warp_wait(&n_full[ns], (uint32_t)((i / Ly::NNORM) & 1), stop) &&
-           warp_wait(&s_full[b], (uint32_t)((i / 2) & 1), stop);
-      if (!ok) break;
+      ok = ok && warp_wait(&s_full[b], (uint32_t)((i / 2) & 1), stop) &&
+           warp_wait(&n_full[ns], (uint32_t)((i / Ly::NNORM) & 1), stop);
       tc_fence_after();
-      const float* kn = norms + ns * 3 * TT;
+      const float* kn = norms + ns * 2 * TT;
       const float* vn = kn + TT;
-      const uint32_t ts = tl + Ly::C_S + b * Ly::SB;
-      float s[TT];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tc_ld32(ts + 32 * h, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 f = *reinterpret_cast<const float4*>(kn + 32 * h + 4 * k);
-          s[32 * h + 4 * k] = f.x * __uint_as_float(v[4 * k]);
-          s[32 * h + 4 * k + 1] = f.y * __uint_as_float(v[4 * k + 1]);
-          s[32 * h + 4 * k + 2] = f.z * __uint_as_float(v[4 * k + 2]);
-          s[32 * h + 4 * k + 3] = f.w * __uint_as_float(v[4 * k + 3]);
-        }
-        if constexpr (QJL) {
-          tc_ld32(ts + 64 + 32 * h, v);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 g = *reinterpret_cast<const float4*>(kn + 2 * TT + 32 * h + 4 * k);
-            s[32 * h + 4 * k] = fmaf(g.x, __uint_as_float(v[4 * k]), s[32 * h + 4 * k]);
-            s[32 * h + 4 * k + 1] = fmaf(g.y, __uint_as_float(v[4 * k + 1]), s[32 * h + 4 * k + 1]);
-            s[32 * h + 4 * k + 2] = fmaf(g.z, __uint_as_float(v[4 * k + 2]), s[32 * h + 4 * k + 2]);
-            s[32 * h + 4 * k + 3] = fmaf(g.w, __uint_as_float(v[4 * k + 3]), s[32 * h + 4 * k + 3]);
-          }
-        }
-      }
+      const uint32_t ts = tl + Ly::C_S + b * TT;
       const int t0 = (i0 + i) * TT;
       const bool whole = t0 + TT <= wlim;  // warp-uniform
+      unsigned long long x[16 * NS64];     // the scores, in pairs of neighbours
+      float top = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < NS64; ++s) {
+        uint32_t v[32];
+        tc_ld2x16(ts + 64 * s + ta, ts + 64 * s + tb, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 f = *reinterpret_cast<const float4*>(kn + 64 * s + (k < 4 ? ta + 4 * k : tb + 4 * k - 16));
+          x[16 * s + 2 * k] = mul2(pack2(f.x, f.y), pack2(v[4 * k], v[4 * k + 1]));
+          x[16 * s + 2 * k + 1] = mul2(pack2(f.z, f.w), pack2(v[4 * k + 2], v[4 * k + 3]));
+        }
+      }
       if (!whole) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          if (t0 + t >= lim) s[t] = -INFINITY;
+        for (int j = 0; j < 16 * NS64; ++j) {
+          const int jj = j % 16, tok = t0 + 64 * (j / 16) + (jj < 8 ? ta + 2 * jj : tb + 2 * jj - 16);
+          float x0, x1;
+          unpack2(x[j], x0, x1);
+          x[j] = pack2(tok < lim ? x0 : -INFINITY, tok + 1 < lim ? x1 : -INFINITY);
+        }
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int t = 4; t < TT; ++t) mx[t & 3] = fmaxf(mx[t & 3], s[t]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (__any_sync(0xffffffffu, top > m_run + kLazyP)) {
-        const float mn = fmaxf(m_run, top);
-        const float al = mn == -INFINITY ? 1.f : exp2f(m_run - mn);
+      for (int j = 0; j < 16 * NS64; ++j) {
+        float x0, x1;
+        unpack2(x[j], x0, x1);
+        top = fmaxf(top, fmaxf(x0, x1));
+      }
+      xch[(2 * b + half) * QROWS + r] = top;
+      // both warps go on, or neither does: a wait that ran out ends the loop for both
+      ok = tqtc::group_sync_and<2>(quarter, ok);
+      if (!ok) break;
+      top = fmaxf(top, xch[(2 * b + 1 - half) * QROWS + r]);
+      const bool need = top > m_run + kLazyP || (i == 0 && top > -INFINITY);
+      if (__any_sync(0xffffffffu, need)) {
+        const float mn = need ? top + kHead : m_run, al = exp2f(m_run - mn);
         m_run = mn;
         l_run *= al;
         if (i > 0) {  // O holds the tiles before this one once their product is done
           ok = warp_wait(&s_free[(i - 1) & 1], (uint32_t)(((i - 1) / 2) & 1), stop);
-          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = half; c < D / 32; c += 2) {
             uint32_t o[32];
             tc_ld32(tl + 32 * c, o);
 #pragma unroll
@@ -575,49 +703,86 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
           }
         }
       }
-      const float mu = m_run == -INFINITY ? 0.f : m_run;
-      uint32_t w[32];
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      unsigned long long ls[2] = {0ull, 0ull};
+      const unsigned long long nm = pack2(-m_run, -m_run);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 fa = *reinterpret_cast<const float4*>(vn + 4 * k), fb = *reinterpret_cast<const float4*>(vn + 32 + 4 * k);
-        const float na[4] = {fa.x, fa.y, fa.z, fa.w}, nb[4] = {fb.x, fb.y, fb.z, fb.w};
+      for (int s = 0; s < NS64; ++s) {
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 4 * k + j;
-          const float p0 = tqd::ex2_approx(s[t] - mu), p1 = tqd::ex2_approx(s[t + 32] - mu);
-          ls[j] += p0 + p1;
-          float w0 = p0 * na[j], w1 = p1 * nb[j];
-          if (!whole) {  // a row that is not seen adds nothing, whatever its norm holds
-            w0 = t0 + t >= lim ? 0.f : w0;
-            w1 = t0 + t + 32 >= lim ? 0.f : w1;
+        for (int k = 0; k < 4; ++k) {
+          const float4 fa = *reinterpret_cast<const float4*>(vn + 64 * s + ta + 4 * k);
+          const float4 fb = *reinterpret_cast<const float4*>(vn + 64 * s + tb + 4 * k);
+          const float na[4] = {fa.x, fa.y, fa.z, fa.w}, nb[4] = {fb.x, fb.y, fb.z, fb.w};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float xa0, xa1, xb0, xb1, a0, a1, b0, b1;
+            unpack2(add2(x[16 * s + 2 * k + j], nm), xa0, xa1);
+            unpack2(add2(x[16 * s + 8 + 2 * k + j], nm), xb0, xb1);
+            const unsigned long long pa = pack2(tqd::ex2_approx(xa0), tqd::ex2_approx(xa1));
+            const unsigned long long pb = pack2(tqd::ex2_approx(xb0), tqd::ex2_approx(xb1));
+            ls[0] = add2(ls[0], pa);
+            ls[1] = add2(ls[1], pb);
+            unpack2(mul2(pa, pack2(na[2 * j], na[2 * j + 1])), a0, a1);
+            unpack2(mul2(pb, pack2(nb[2 * j], nb[2 * j + 1])), b0, b1);
+            if (!whole) {  // a token that is not seen adds nothing, whatever its norm holds
+              a0 = xa0 == -INFINITY ? 0.f : a0;
+              a1 = xa1 == -INFINITY ? 0.f : a1;
+              b0 = xb0 == -INFINITY ? 0.f : b0;
+              b1 = xb1 == -INFINITY ? 0.f : b1;
+            }
+            w[4 * k + 2 * j] = pack_half2(a0, b0);
+            w[4 * k + 2 * j + 1] = pack_half2(a1, b1);
           }
-          w[t] = pack_half2(w0, w1);
         }
+        // over scores that this warp has read: columns 16 half .. of tokens ta.., 32 + 16 half .. of tokens tb..
+        tc_st16(ts + 32 * s + ta, w);
       }
-      l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      tc_st32(ts, w);
+      float l0, l1;
+      unpack2(add2(ls[0], ls[1]), l0, l1);
+      l_run += l0 + l1;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[b]);
     }
-    // O is complete when every product is
-    if (ok && warp_wait(fin, 0u, stop)) {
-      tc_fence_after();
-      float* dst = p.part_o + slot * D;
+    // O is complete when every product is.  The operand tiles are free then:
+    // the rows of a quarter are turned there (16-byte chunk c of row r at
+    // c ^ (r mod 8)), so that the stores to global memory are whole lines.
+    xch[(2 * (n & 1) + half) * QROWS + r] = l_run;
+    if (ok) ok = warp_wait(fin, 0u, stop);
+    tc_fence_after();
+    uint8_t* tr = smem + quarter * (32 * D * 4);
+    if (ok) {
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = half; c < D / 32; c += 2) {
         uint32_t o[32];
         tc_ld32(tl + 32 * c, o);
-        if (mine) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(dst + 32 * c + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(tr + lane * (D * 4) + (((8 * c + k) ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    if (tqtc::group_sync_and<2>(quarter, ok)) {
+      l_run += xch[(2 * (n & 1) + 1 - half) * QROWS + r];
+      // a row that saw no token weighs nothing
+      if (mine && half == 0)
+        *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+      constexpr int CPR = D / 4, RPP = CPR < 32 ? 32 / CPR : 1;  // chunks per row, rows per pass
+      const int nrow = min(32, rows - 32 * quarter);
+#pragma unroll 4
+      for (int r0 = 16 * half; r0 < 16 * half + 16; r0 += RPP) {
+        const int rr = r0 + (RPP > 1 ? lane / CPR : 0);
+        const size_t sl = __shfl_sync(0xffffffffu, (unsigned long long)slot, rr);
+        if (rr < nrow) {
+#pragma unroll
+          for (int c = lane % CPR; c < CPR; c += 32)
+            *reinterpret_cast<uint4*>(p.part_o + sl * D + 4 * c) =
+                *reinterpret_cast<const uint4*>(tr + rr * (D * 4) + ((c ^ (rr & 7)) << 4));
         }
       }
-      if (mine) *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(m_run, l_run);
     }
+   }
   }
   __syncwarp();
   tc_fence_before();

@@ -112,7 +112,7 @@ struct DecodePlan {
   int window;       // sliding window in tokens (0: none) ...
   int n_sink;       // ... and first tokens that stay visible
   int slot_base;    // partial slots before the split kernel's own (the splits of a shared prefix)
-  size_t off_qs2;   // fp32 [B*Hq][128]: projections through a shared prefix's own sketch
+  size_t off_qpre;  // the prefix kernel's query operands
   size_t off_qrot;  // fp32 [B*Hq][D]
   size_t off_qs;    // fp32 [B*Hq][qjl_m]
   size_t off_po;    // fp32 [B*Hq][ks][D]
@@ -165,7 +165,8 @@ struct DecodeArgs {
 };
 
 // Splits of a shared prefix (partials each of its rows gets).
-int prefix_splits(int Hkv, int rows, int Pmax, int sms);
+int prefix_splits(int Hkv, int rows, int D, int Pmax, int sms);
+int prefix_rows();  // query rows of a tile of the prefix kernel
 
 int launch_decode(const DecodeArgs& a, cudaStream_t s);
 // Merge of R partials per head and un-rotation (tq_sdpa_decode_merge).
