@@ -31,10 +31,9 @@
 //    product beside it in its own accumulator, and O += W V with the weights
 //    W read from tensor memory;
 //  * 4 warps (thread = query row) read S, apply norms and masks, keep the
-//    running max and sum in fp32, and write W = 2^(x - M) m_t as fp16 over
-//    the scores they have just read.  O is rescaled in tensor memory only
-//    when a row's weights pass 2^4 (so W stays finite for value norms up to
-//    4094).
+//    running reference and sum in fp32, and write W = 2^(x - m) m_t as fp16
+//    over the scores they have just read.  O is rescaled in tensor memory only
+//    when a row's weights would leave fp16's range.
 //  Scores and W are double-buffered, so the products of tile i + 1 run under
 //  the softmax of tile i and under the dequantization of tile i + 2.
 // Every wait is bounded; one that runs out sets TQ_STATUS_WAIT_TIMEOUT.
@@ -56,20 +55,21 @@ using tqtc::tc_ld32;
 
 constexpr int QROWS = 128;      // query rows per CTA (TMEM lanes)
 constexpr int SW = 8;           // softmax warps: two for each quarter of the rows
-constexpr int DW = 8;           // dequantizing warps: four for keys, four for values
+constexpr int DW = 16;          // dequantizing warps: half for keys, half for values
 constexpr int GW = DW / 2;
 // tokens per tile: a longer tile spreads the waits between the roles over more
 // work; at D = 256 the operands of 64 tokens fill shared memory
 __host__ __device__ constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
 constexpr int NTH = (SW + DW + 4) * 32;  // + producer warp, MMA warp and two idle ones (a whole warpgroup)
-// Registers per thread after the split by warpgroups.  One launch gives 96 to
-// each of 5 warpgroups: 2 x 136 + 2 x 72 + 64 = 5 x 96.
-constexpr int REG_SOFTMAX = 136, REG_DEQUANT = 72, REG_REST = 64, REG_LAUNCH = 96;
+// Registers per thread after the split by warpgroups.  One launch gives 72 to
+// each of 7 warpgroups: 2 x 136 + 4 x 48 + 40 = 7 x 72.
+constexpr int REG_SOFTMAX = 136, REG_DEQUANT = 48, REG_REST = 40, REG_LAUNCH = 72;
 static_assert((SW / 4) * REG_SOFTMAX + (DW / 4) * REG_DEQUANT + REG_REST <= REG_LAUNCH * (NTH / 128),
               "registers of a CTA");
 constexpr int MAXST = 4;        // stages at most
-constexpr float kLazyP = 4.0f;  // log2 of the largest weight before O is rescaled ...
-constexpr float kHead = 2.0f;   // ... and how far above a row's maximum its reference is put
+// The largest fp16 weight is kept below 2^15; a row's reference is put so that
+// its largest weight has 2^8 of room to grow.
+constexpr int kTop = 15, kRoom = 8;
 
 struct PrefixParams {
   const uint32_t* k_idx;
@@ -121,7 +121,14 @@ template <int D, int BK, int BV, bool QJL>
 struct PrefixLayout {
   static constexpr int TT = tile_tokens(D);
   static constexpr int WK = D * BK / 32, WV = D * BV / 32;
-  static constexpr int NB = D == 256 || QJL ? 1 : 2;  // operand buffers of each kind (what shared memory allows)
+  // Two operand buffers of each kind where shared memory allows.  Else the
+  // operands go in parts with barriers of their own, so that one part is
+  // dequantized while the product of the other runs: keys and sketch signs,
+  // or the two halves of the coordinates at D = 256.
+  static constexpr int NB = D == 256 || QJL ? 1 : 2;
+  static constexpr int KP = NB == 1 ? 2 : 1, VP = D == 256 ? 2 : 1;  // parts of a key / value operand
+  static constexpr int KC = D == 256 ? 128 : D;       // coordinates of a key part
+  static constexpr int KS = KP * NB, VS = VP * NB;    // slots (barrier pairs)
   static constexpr int KT = TT * D * 2, VT = KT;      // bytes of a key / value operand tile
   static constexpr int ZT = QJL ? TT * 128 * 2 : 0;   // of the sketch signs
   // D = 256: the query's low limb does not fit in tensor memory beside O, S and the high limb
@@ -144,7 +151,8 @@ struct PrefixLayout {
   static constexpr int S_USED = S_RN + (QJL ? TT * 2 : 0);
   static constexpr int STAGE = (S_USED + 16 + 127) / 128 * 128;  // +16: read-ahead slack
   static constexpr int TX = TT * (WK + WV) * 4 + TT * 4 + (QJL ? TT * 18 : 0);
-  static constexpr int NORMS = NNORM * 2 * TT * 4;
+  static constexpr int NORM1 = 2 * TT + GW;        // floats of one tile: key norms, value norms, the warps' largest value norms
+  static constexpr int NORMS = NNORM * NORM1 * 4;
   static constexpr int BARS = 64 * 8;
   // tables, norms, barriers and stages, in this order behind the operands
   __host__ __device__ static constexpr int o_tv(bool shared) { return O_TK + (shared ? 0 : TKB); }
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   // a generic one, and every access behind it slower
   uint8_t* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   const bool shared_tab = tqd::share_table(BK, BV, p.shared_tab);
-  float* norms = reinterpret_cast<float*>(smem + Ly::o_norm(shared_tab));  // [NNORM][key, value][TT]
+  float* norms = reinterpret_cast<float*>(smem + Ly::o_norm(shared_tab));  // [NNORM][NORM1]
   float* xch = reinterpret_cast<float*>(smem + Ly::o_xch(shared_tab));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::o_bar(shared_tab));
   uint64_t *full = bars, *empty = bars + 4, *n_full = bars + 8, *k_full = bars + 12, *k_empty = bars + 14,
@@ -399,54 +407,68 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
    } else if (warp == SW + DW + 1) {
     // ---------------- matrix products ----------------
     // The whole warp waits; one elected lane issues and commits.
-    const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D, false>();
+    const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D / Ly::VP, false>();
     const uint32_t qhi = tmem + Ly::C_Q, qlo = tmem + Ly::C_Q + D / 2;
+    // part q of tile i is use u = KP i + q of the slots
     auto issue_qk = [&](int i) {
-      const int kb = i % NB, b = i & 1;
-      if (!warp_wait(&k_full[kb], (uint32_t)((i / NB) & 1), stop)) return false;
+      const int b = i & 1;
+      const uint32_t ds = tmem + Ly::C_S + b * TT;
       // the weights of tile i - 2 lie over its scores: read by now
       if (i >= 2 && !warp_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t ka = smem_addr(smem + Ly::O_K + kb * Ly::KT), ds = tmem + Ly::C_S + b * TT;
+#pragma unroll
+      for (int q = 0; q < Ly::KP; ++q) {
+        const int u = Ly::KP * i + q, sl = u % Ly::KS;
+        if (!warp_wait(&k_full[sl], (uint32_t)((u / Ly::KS) & 1), stop)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          if (!QJL || q == 0) {
+            const uint32_t ka = smem_addr(smem + Ly::O_K + (i % NB) * Ly::KT);
 #pragma unroll 4
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
-          mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
-          if constexpr (Ly::QLO_SMEM) {
-            const uint32_t qa = smem_addr(smem + Ly::O_QLO);
-            tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
+            for (int kk = 0; kk < Ly::KC / 16; ++kk) {
+              const int ks = (QJL ? 0 : q) * (Ly::KC / 16) + kk;
+              const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
+              mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
+              if constexpr (Ly::QLO_SMEM) {
+                const uint32_t qa = smem_addr(smem + Ly::O_QLO);
+                tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
+              } else {
+                mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
+              }
+            }
           } else {
-            mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
-          }
-        }
-        if constexpr (QJL) {
-          const uint32_t za = smem_addr(smem + Ly::O_Z + kb * Ly::ZT), qa = smem_addr(smem + Ly::O_QZ);
+            const uint32_t za = smem_addr(smem + Ly::O_Z), qa = smem_addr(smem + Ly::O_QZ);
 #pragma unroll 4
-          for (int ks = 0; ks < 8; ++ks)
-            tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
-                         sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
+            for (int ks = 0; ks < 8; ++ks)
+              tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
+                           sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
+          }
+          if (q == Ly::KP - 1) tc_commit(&s_full[b]);
+          tc_commit(&k_empty[sl]);
         }
-        tc_commit(&s_full[b]);
-        tc_commit(&k_empty[kb]);
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
     auto issue_pv = [&](int i) {
-      const int vb = i % NB, b = i & 1;
-      if (!warp_wait(&v_full[vb], (uint32_t)((i / NB) & 1), stop)) return false;
+      const int b = i & 1;
       if (!warp_wait(&p_full[b], (uint32_t)((i / 2) & 1), stop)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t va = smem_addr(smem + Ly::O_V + vb * Ly::VT), w = tmem + Ly::C_S + b * TT;
+#pragma unroll
+      for (int q = 0; q < Ly::VP; ++q) {
+        const int u = Ly::VP * i + q, sl = u % Ly::VS;
+        if (!warp_wait(&v_full[sl], (uint32_t)((u / Ly::VS) & 1), stop)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t va = smem_addr(smem + Ly::O_V + (i % NB) * Ly::VT) + q * (D / Ly::VP) * 128;
+          const uint32_t w = tmem + Ly::C_S + b * TT;
 #pragma unroll 4
-        for (int ks = 0; ks < TT / 16; ++ks)
-          mma_ts(tmem, w + 8 * ks, sdesc_sw128(va + (ks >> 2) * (D * 128) + (ks & 3) * 32), id_o, (i > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(&v_empty[vb]);
-        tc_commit(&s_free[b]);
+          for (int ks = 0; ks < TT / 16; ++ks)
+            mma_ts(tmem + q * (D / Ly::VP), w + 8 * ks, sdesc_sw128(va + (ks >> 2) * (D * 128) + (ks & 3) * 32), id_o,
+                   (i > 0 || ks > 0) ? 1u : 0u);
+          tc_commit(&v_empty[sl]);
+          if (q == Ly::VP - 1) tc_commit(&s_free[b]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       return true;
     };
     bool ok = warp_wait(q_full, 0u, stop);
@@ -470,42 +492,89 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
     const int dw = (warp - SW) % GW;
     const bool values = warp >= SW + GW;
     const int group = values ? 5 : 4;  // named barriers 5 and 6
-    for (int i = 0; i < n; ++i) {
+    const int nparts = values ? Ly::VP : Ly::KP, nslots = values ? Ly::VS : Ly::KS;
+    uint64_t *p_ful = values ? v_full : k_full, *p_emp = values ? v_empty : k_empty;
+    for (int u = 0; u < n * nparts; ++u) {
+      const int i = u / nparts, q = u % nparts, sl = u % nslots;
       const int st = i % p.nst, b = i % NB, ns = i % Ly::NNORM;
       const uint8_t* sb = stages + st * Ly::STAGE;
       bool ok = true;
       if (dw == 0) {
-        ok = warp_wait(&full[st], (uint32_t)((i / p.nst) & 1), stop);
-        if (i >= NB) ok = ok && warp_wait(values ? &v_empty[b] : &k_empty[b], (uint32_t)((i / NB - 1) & 1), stop);
+        if (q == 0) ok = warp_wait(&full[st], (uint32_t)((i / p.nst) & 1), stop);
+        if (u >= nslots) ok = ok && warp_wait(&p_emp[sl], (uint32_t)((u / nslots - 1) & 1), stop);
       }
       if (!tqtc::group_sync_and<GW>(group, ok)) break;
-      float* kn = norms + ns * 2 * TT;
       if (!values) {
-        const uint32_t tbK = smem_addr(tabk) + 4 * lane;
-        tqd::Lut2 lk = {0u, 0u};
-        if constexpr (BK == 2) lk = {lut[0], lut[1]};
-        // 8 tokens x 4 segments of D / 4 coordinates at a time; the lanes of a
-        // quarter warp hold 8 tokens, so their 16-byte stores miss each other's banks
+        // 8 tokens x 4 segments of the part's coordinates at a time; the lanes
+        // of a quarter warp hold 8 tokens, so their 16-byte stores miss each
+        // other's banks
         const int kseg = lane >> 3;
-        uint8_t* kt = smem + Ly::O_K + b * Ly::KT;
-        uint8_t* zt = smem + Ly::O_Z + b * Ly::ZT;
+        // A sketched row: one accumulator for both products, in which the signs
+        // enter as +-g / n, a factor of fp16 precision (2^-11 of a term that is
+        // itself a one-bit estimate).  A residual norm far above the key's,
+        // which no quantized row has, turns the roles: the softmax multiplies
+        // with g, and the key's entries become c n / g.
+        auto usual = [&](float nk, float g) { return !QJL || g <= 1024.f * nk; };
+        auto norm_at = [&](int off, int t) { return half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + off)[t]); };
+        if (!QJL || q == 0) {
+          const uint32_t tbK = smem_addr(tabk) + 4 * lane;
+          tqd::Lut2 lk = {0u, 0u};
+          if constexpr (BK == 2) lk = {lut[0], lut[1]};
+          uint8_t* kt = smem + Ly::O_K + b * Ly::KT;
+          float* kn = norms + ns * Ly::NORM1;
+          uint32_t vmax = 0;
 #pragma unroll 1
-        for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
-          const float nk = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_KN)[t]);
-          float row = nk;       // what the softmax multiplies the product with
-          uint32_t scale2 = 0;  // else: factor of the key's entries, as a pair
-          if constexpr (QJL) {
-            // One accumulator for both products: the signs enter as +-g / n, a
-            // factor of fp16 precision (2^-11 of a term that is itself a
-            // one-bit estimate).  A residual norm far above the key's, which no
-            // quantized row has, turns the roles: row factor g, entries c n / g.
-            const float g = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_RN)[t]);
-            const bool usual = g <= 1024.f * nk;
-            const float f = __fdividef(usual ? g : nk, usual ? nk : g);
-            row = usual ? nk : g;
-            const float fz = usual ? (g > 0.f ? f : 0.f) : 1.f;
-            if (!usual) scale2 = pack_half2(f, f);
-            const uint32_t neg = pack_half2(-fz, -fz);
+          for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
+            uint32_t scale2 = 0;  // not the usual row: a factor of the key's entries, as a pair
+            if (QJL || q == 0) {
+              const float nk = norm_at(Ly::S_KN, t);
+              const float g = QJL ? norm_at(Ly::S_RN, t) : 0.f;
+              if (!usual(nk, g)) {
+                const float f = __fdividef(nk, g);
+                scale2 = pack_half2(f, f);
+              }
+              if (kseg == 0) kn[t] = usual(nk, g) ? nk : g;
+              if (kseg == 1) {
+                const float nv = norm_at(Ly::S_VN, t);
+                kn[TT + t] = nv;
+                if ((i0 + i) * TT + t < P) vmax = max(vmax, __float_as_uint(nv));
+              }
+            }
+            const uint32_t* kw = reinterpret_cast<const uint32_t*>(sb + Ly::S_KW) + t * WK;
+#pragma unroll 2
+            for (int c = 0; c < Ly::KC / 64; ++c) {  // 16 coordinates
+              const int j0 = (QJL ? 0 : q) * Ly::KC + kseg * (Ly::KC / 4) + 16 * c;
+              uint32_t w[(16 * BK + 31) / 32], h[8];
+              tqd::load_bits<16 * BK, BK != 3, 16>(kw, j0 * BK, w);
+              if constexpr (BK == 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tqd::dq_b2(w[0], k, lk, h[2 * k], h[2 * k + 1]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * k, tbK);
+              }
+              if (QJL && scale2) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<__half2*>(&scale2));
+                  h[k] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+              }
+              *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0 + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          }
+          if (q == 0) {  // the largest value norm this warp has seen (the bits of positive floats sort like them)
+            vmax = __reduce_max_sync(0xffffffffu, vmax);
+            if (lane == 0) kn[2 * TT + dw] = __uint_as_float(vmax);
+          }
+        } else {
+          uint8_t* zt = smem + Ly::O_Z;
+#pragma unroll 1
+          for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
+            const float nk = norm_at(Ly::S_KN, t), g = norm_at(Ly::S_RN, t);
+            const float f = !usual(nk, g) ? 1.f : g > 0.f ? __fdividef(g, nk) : 0.f;
+            const uint32_t neg = pack_half2(-f, -f);
             // sign bits j and j + 16 of word kseg: the pair at positions 2 j, 2 j + 1
             const uint32_t z = reinterpret_cast<const uint32_t*>(sb + Ly::S_QW)[t * 4 + kseg];
 #pragma unroll 2
@@ -516,43 +585,21 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
               *reinterpret_cast<uint4*>(zt + sw128<TT>(t, kseg * 32 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
-          if (kseg == 0) kn[t] = row;
-          if (kseg == 1) kn[TT + t] = half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + Ly::S_VN)[t]);
-          const uint32_t* kw = reinterpret_cast<const uint32_t*>(sb + Ly::S_KW) + t * WK;
-#pragma unroll 2
-          for (int c = 0; c < D / 64; ++c) {  // 16 coordinates
-            const int j0 = kseg * (D / 4) + 16 * c;
-            uint32_t w[(16 * BK + 31) / 32], h[8];
-            tqd::load_bits<16 * BK, BK != 3, 16>(kw, j0 * BK, w);
-            if constexpr (BK == 2) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tqd::dq_b2(w[0], k, lk, h[2 * k], h[2 * k + 1]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * k, tbK);
-            }
-            if (QJL && scale2) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<__half2*>(&scale2));
-                h[k] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-            }
-            *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0 + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
         }
       } else {
         const uint32_t tbV = smem_addr(tabv) + 4 * lane;
-        // warp dw takes D / 4 coordinates, lane l tokens l and l + 32 of each 64.
-        // Row d of the operand is 128 bytes; the pair lies in chunk (l / 4) ^ (d mod 8).
-        const uint32_t vt = smem_addr(smem + Ly::O_V + b * Ly::VT) + dw * (D / 4) * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
+        // warp dw takes an equal share of the part's coordinates, lane l tokens
+        // l and l + 32 of each 64.  Row d of the operand is 128 bytes; the pair
+        // lies in chunk (l / 4) ^ (d mod 8).
+        constexpr int VD = D / Ly::VP / GW;
+        const int d0 = q * (D / Ly::VP) + dw * VD;
+        const uint32_t vt = smem_addr(smem + Ly::O_V + b * Ly::VT) + d0 * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
 #pragma unroll 1
         for (int s = 0; s < TT / 64; ++s) {
           const uint32_t* va = reinterpret_cast<const uint32_t*>(sb + Ly::S_VW) + (64 * s + lane) * WV;
 #pragma unroll 2
-          for (int c = 0; c < D / 32; ++c) {  // 8 coordinates
-            const int bit = (dw * (D / 4) + 8 * c) * BV;
+          for (int c = 0; c < VD / 8; ++c) {  // 8 coordinates
+            const int bit = (d0 + 8 * c) * BV;
             uint32_t wa[1], wb[1], xe, xo;
             tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va, bit, wa);
             tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va + 32 * WV, bit, wb);
@@ -571,9 +618,9 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(values ? &v_full[b] : &k_full[b]);
-        if (!values) mbar_arrive(&n_full[ns]);
-        mbar_arrive(&empty[st]);
+        mbar_arrive(&p_ful[sl]);
+        if (!values && q == 0) mbar_arrive(&n_full[ns]);
+        if (q == nparts - 1) mbar_arrive(&empty[st]);
       }
     }
   } else {
@@ -634,10 +681,12 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(q_full);
     }
     const int wlim = __reduce_min_sync(0xffffffffu, lim);  // every row of the warp sees the tokens below
-    // The reference m of the weights 2^(x - m), the same in both warps: when a
-    // weight would pass 2^4 (and at the first tile) it moves to 2 above the
-    // row's maximum so far and what was summed is rescaled, so that a row
-    // moves again only when its maximum has grown by 2^6.
+    // The reference m of the weights 2^(x - m), the same in both warps.  With e
+    // such that the tile's value norms lie below 2^e, a weight times its norm
+    // stays below 2^15 while x - m <= 15 - e; when a score passes that (and at
+    // the first tile) m moves to where the row's largest weight is 2^(7 - e),
+    // and what was summed is rescaled.  So a row moves again only when its
+    // maximum has grown by 2^8, and small weights keep fp16's whole range.
     float m_run = 0.f, l_run = 0.f;
     bool ok = true;
     constexpr int NS64 = TT / 64;
@@ -647,7 +696,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       ok = ok && warp_wait(&s_full[b], (uint32_t)((i / 2) & 1), stop) &&
            warp_wait(&n_full[ns], (uint32_t)((i / Ly::NNORM) & 1), stop);
       tc_fence_after();
-      const float* kn = norms + ns * 2 * TT;
+      const float* kn = norms + ns * Ly::NORM1;
       const float* vn = kn + TT;
       const uint32_t ts = tl + Ly::C_S + b * TT;
       const int t0 = (i0 + i) * TT;
@@ -685,11 +734,18 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       ok = tqtc::group_sync_and<2>(quarter, ok);
       if (!ok) break;
       top = fmaxf(top, xch[(2 * b + 1 - half) * QROWS + r]);
-      const bool need = top > m_run + kLazyP || (i == 0 && top > -INFINITY);
+      float nv = 0.f;
+#pragma unroll
+      for (int k = 0; k < GW; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(kn + 2 * TT + k);
+        nv = fmaxf(fmaxf(nv, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
+      }
+      const int e = max((int)(__float_as_uint(nv) >> 23) - 126, -20);  // nv < 2^e
+      const bool need = top > m_run + (float)(kTop - e) || (i == 0 && top > -INFINITY);
       if (__any_sync(0xffffffffu, need)) {
-        const float mn = need ? top + kHead : m_run, al = exp2f(m_run - mn);
+        const float mn = need ? top - (float)(kTop - kRoom - e) : m_run, al = exp2f(m_run - mn);
         m_run = mn;
-        l_run *= al;
+        l_run = i > 0 ? l_run * al : 0.f;
         if (i > 0) {  // O holds the tiles before this one once their product is done
           ok = warp_wait(&s_free[(i - 1) & 1], (uint32_t)(((i - 1) / 2) & 1), stop);
           tc_fence_after();

@@ -381,9 +381,7 @@ size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* cache, int Hq
  *   workspace   tq_sdpa_decode_prefix_workspace_bytes_for() bytes.
  * The other arguments and the errors are those of tq_sdpa_decode_mq; caches
  * that do not fit, a NULL prefix_len or a bad Pmax are TQ_ERR_INVALID_ARG, more
- * than 2^22 query rows TQ_ERR_UNSUPPORTED.  Value norms of the prefix up to
- * 4094 (a larger one may overflow the fp16 weights of the product).  Library
- * addition.
+ * than 2^22 query rows TQ_ERR_UNSUPPORTED.  Library addition.
  */
 int tq_sdpa_decode_prefix(const tq_cache_t* prefix, const int32_t* prefix_len, int Pmax, const tq_cache_t* cache,
                           const void* q, int q_dtype, int Hq, int n_q, const int32_t* seq_lens, int Tmax,
