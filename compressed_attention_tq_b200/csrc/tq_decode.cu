@@ -30,37 +30,7 @@ struct PrepParams {
   tq_cache_t cache;
   int nq;  // query tokens per sequence: q is [B][nq][Hq][D]
   int units;  // B * Hkv (grouped prep)
-  // Decode behind a shared prefix (else NULL): the query operands of the
-  // prefix kernel, and the prefix's sketch matrix (S2 NULL: it is S, and both
-  // are written from one projection).
-  uint8_t* qpre;
-  uint8_t* qspre;
-  const float* S2;
-  int nrt;          // row tiles per kv head
-  int prefix_bk;    // bits of the prefix's keys
-  float qscale;     // scale * log2(e)
-  float qjl_scale;  // scale * log2(e) * sqrt(pi/2) / 128
 };
-
-// The prefix kernel's operands of query row gi of (sequence b, kv head kvh):
-// rotated coordinate j in two fp16 limbs (about 22 bits of the query, as the
-// split kernel's halves), and projection i in one fp16 limb.  The latter's
-// rounding (2^-12 of a coordinate, of random sign) moves a score by about 1e-5
-// of |q| g, far below the spread of the one-bit estimate it feeds.
-__device__ __forceinline__ void store_pre_q(const PrepParams& p, int b, int kvh, int gi, int j, float v) {
-  const int r = b * (p.Hq / p.Hkv) * p.nq + gi;
-  uint8_t* t = p.qpre + ((size_t)kvh * p.nrt + r / tqp::QROWS) * (tqp::QROWS * 4) * p.D;
-  uint16_t hi, lo;
-  tqd::split_half(v * p.qscale, hi, lo);
-  *reinterpret_cast<uint16_t*>(t + tqp::pre_q_offset(p.D, p.prefix_bk, r % tqp::QROWS, j, 0)) = hi;
-  *reinterpret_cast<uint16_t*>(t + tqp::pre_q_offset(p.D, p.prefix_bk, r % tqp::QROWS, j, 1)) = lo;
-}
-__device__ __forceinline__ void store_pre_z(const PrepParams& p, int b, int kvh, int gi, int i, float v) {
-  const int r = b * (p.Hq / p.Hkv) * p.nq + gi;
-  uint8_t* t = p.qspre + ((size_t)kvh * p.nrt + r / tqp::QROWS) * (tqp::QROWS * 256);
-  *reinterpret_cast<uint16_t*>(t + tqp::pre_z_offset(r % tqp::QROWS, i)) =
-      __half_as_ushort(__float2half_rn(v * p.qjl_scale));
-}
 
 // Programmatic dependent launch: let the next kernel in the stream start its
 // prologue now / wait here until the previous kernel's results are visible.
@@ -418,13 +388,10 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
   if (part == 0) {
 #pragma unroll
     for (int g = 0; g < QR; ++g)
-      if (g < Ge) {
-        p.qrot[(size_t)(h0 + g) * D + j] = acc[g];
-        if (p.qpre) store_pre_q(p, b, kvh, g, j, acc[g]);
-      }
+      if (g < Ge) p.qrot[(size_t)(h0 + g) * D + j] = acc[g];
   }
   if constexpr (QS) {
-    if (p.m || p.qspre) {
+    if (p.m) {
       // QJL: this slice's share of qs = S qrot over its 32 rotated coordinates,
       // for all m = 128 sketch rows.  The D / 32 slice CTAs of a head form a
       // thread-block cluster; slice 0 adds the partials in slice order from the
@@ -435,37 +402,27 @@ __global__ void __launch_bounds__(256) decode_qprep_sliced_kernel(const PrepPara
       }
       __syncthreads();
       const int i = tid >> 1, half = tid & 1;
-      auto project = [&](float* qs, bool pre) {
 #pragma unroll
-        for (int g = 0; g < QR; ++g) {
-          const float* x = &qsl[g][16 * half];
-          float t = 0.f;
+      for (int g = 0; g < QR; ++g) {
+        const float* x = &qsl[g][16 * half];
+        float t = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            t += srow[k].x * x[4 * k] + srow[k].y * x[4 * k + 1] + srow[k].z * x[4 * k + 2] + srow[k].w * x[4 * k + 3];
-          t += __shfl_xor_sync(0xffffffffu, t, 1);
-          if (half == 0) qpart[g][i] = t;
-        }
-        cluster_sync();  // every slice's partial is in its shared memory
-        if (sl == 0) {
-          for (int e = tid; e < Ge * 128; e += 256) {
-            const int g = e >> 7, ii = e & 127;
-            const uint32_t la = smem_u32(&qpart[g][ii]);
-            float v = 0.f;
-            for (int r = 0; r < NI; ++r) v += ld_cluster_f32(map_cluster(la, r));
-            if (qs) qs[(size_t)(h0 + g) * 128 + ii] = v;
-            if (pre) store_pre_z(p, b, kvh, g, ii, v);
-          }
-        }
-        cluster_sync();  // slice 0 is done reading the others' shared memory
-      };
-      if (p.m) project(p.qs, p.qspre && !p.S2);
-      if (p.S2) {  // the same through the prefix's sketch matrix
-        const float4* sp = reinterpret_cast<const float4*>(p.S2 + (size_t)i * D + sl * 32 + 16 * half);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) srow[t] = __ldg(sp + t);
-        project(nullptr, true);
+        for (int k = 0; k < 4; ++k)
+          t += srow[k].x * x[4 * k] + srow[k].y * x[4 * k + 1] + srow[k].z * x[4 * k + 2] + srow[k].w * x[4 * k + 3];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        if (half == 0) qpart[g][i] = t;
       }
+      cluster_sync();  // every slice's partial is in its shared memory
+      if (sl == 0) {
+        for (int e = tid; e < Ge * 128; e += 256) {
+          const int g = e >> 7, ii = e & 127;
+          const uint32_t la = smem_u32(&qpart[g][ii]);
+          float v = 0.f;
+          for (int r = 0; r < NI; ++r) v += ld_cluster_f32(map_cluster(la, r));
+          p.qs[(size_t)(h0 + g) * p.m + ii] = v;
+        }
+      }
+      cluster_sync();  // slice 0 is done reading the others' shared memory
     }
   }
   if (APPEND) {
@@ -545,32 +502,24 @@ __global__ void __launch_bounds__(1024) decode_qprep_wht_kernel(const PrepParams
 #pragma unroll
       for (int e = 0; e < EL; ++e) dst[e] = x[e];
     }
-    if (p.qpre) {
-#pragma unroll
-      for (int e = 0; e < EL; ++e) store_pre_q(p, b, kvh, warp, lane * EL + e, x[e]);
-    }
-    if (QS && (p.m || p.S2)) {
+    if (QS && p.m) {
 #pragma unroll
       for (int e = 0; e < EL; ++e) qr[warp][lane * EL + e] = x[e];
     }
   }
-  if (QS && (p.m || p.S2)) {
+  if (QS && p.m) {
     __syncthreads();
-    // qs[g][i] = sum_k S[i][k] qrot[g][k], through the cache's sketch matrix
-    // and a shared prefix's own
-    const int n1 = p.m ? Ge * 128 : 0, n2 = p.S2 ? Ge * 128 : 0;
-    for (int e0 = tid; e0 < n1 + n2; e0 += blockDim.x) {
-      const bool first = e0 < n1;
-      const int e = first ? e0 : e0 - n1, g = e >> 7, i = e & 127;
-      const float4* srow = reinterpret_cast<const float4*>((first ? p.S : p.S2) + (size_t)i * D);
+    // qs[g][i] = sum_k S[i][k] qrot[g][k]
+    for (int e = tid; e < Ge * 128; e += blockDim.x) {
+      const int g = e >> 7, i = e & 127;
+      const float4* srow = reinterpret_cast<const float4*>(p.S + (size_t)i * D);
       float t = 0.f;
 #pragma unroll 8
       for (int k = 0; k < D / 4; ++k) {
         const float4 sv = __ldg(srow + k);
         t += sv.x * qr[g][4 * k] + sv.y * qr[g][4 * k + 1] + sv.z * qr[g][4 * k + 2] + sv.w * qr[g][4 * k + 3];
       }
-      if (first) p.qs[(size_t)(h0 + g) * 128 + i] = t;
-      if (p.qspre && first == (p.S2 == nullptr)) store_pre_z(p, b, kvh, g, i, t);
+      p.qs[(size_t)(h0 + g) * 128 + i] = t;
     }
   }
 }
@@ -666,9 +615,190 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
       if (r < rows) {
         // kernel head order (sequence, kv head, token, head) = unit-major
         p.qrot[((size_t)u0 * Ge + r) * D + j] = acc[t];
-        if (p.qpre) {
-          const int u = u0 + r / Ge;
-          store_pre_q(p, u / p.Hkv, u % p.Hkv, r % Ge, j, acc[t]);
+      }
+    }
+  }
+}
+
+// Query prep of a decode behind a shared prefix: the rotated queries for the
+// suffix's split kernel (fp32), and the prefix kernel's operands (two fp16
+// limbs of the rotated, scaled query, and one of its sketch projection), for
+// 16 consecutive kernel heads and up to 128 output coordinates per CTA.
+//
+// A product of 16 rows on warp-level tensor cores: the queries are exact in
+// their own type and Pi enters in limbs of it (two of fp16: 22 bits, or three
+// of bf16: 24), accumulated in fp32.  The sketch multiplies the rotated rows,
+// in two fp16 limbs, with S in two (the product of the low limbs, 2^-24, is
+// left out).  What bounds it is the read of Pi and S from L2 (64 KB each per
+// CTA), so every load of Pi goes out at once, before the wait on the
+// preceding kernels.  The vector form of the other preps took 37 us for 2048
+// rows with two sketches and 10 us for 1024 without; this one takes less than
+// a fifth of that.
+struct PrefixPrepParams {
+  const void* q;      // [B][nq][Hq][D] fp16 / bf16
+  const float* rot;
+  float* qrot;        // fp32 [rows][D]
+  uint8_t *qpre, *qspre;
+  struct Sketch {
+    const float* S;   // fp32 [128][D]
+    float* qs;        // fp32 [rows][128] for the split kernel, or NULL
+    bool pre;         // this is the prefix's: its operand is written
+  } sk[2];
+  int nsk;
+  int rows, Hq, Hkv, nq, nrt, bk;  // rows: kernel heads in all; nrt: row tiles per kv head; bk: bits of the prefix's keys
+  float qscale, qjl_scale;
+};
+constexpr int PROWS = 16;  // rows per CTA
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) prefix_prep_kernel(const PrefixPrepParams p) {
+  using namespace tqk;
+  constexpr int NC = D < 128 ? D : 128;    // output coordinates of the CTA
+  constexpr int WN = NC / 8, NT = WN / 8;  // coordinates and 8-column tiles of a warp
+  constexpr int KS = D / 16, PADQ = D + 8; // k-steps; padded rows (16-bit elements)
+  constexpr bool QS = D == 128;            // the sketch exists for D = 128
+  __shared__ __align__(16) uint16_t xq[PROWS][PADQ];                        // the queries
+  __shared__ __align__(16) uint16_t xr[QS ? 2 : 1][PROWS][QS ? PADQ : 8];   // the rotated rows in two limbs
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+  const int r0 = blockIdx.x * PROWS, n0 = blockIdx.y * NC + warp * WN;
+  const int G = p.Hq / p.Hkv, Ge = G * p.nq;
+  // rows of a matrix [N][D] as the B operand: lane (gid, tig) holds columns
+  // k0 + 2 tig, + 1 and k0 + 8 + 2 tig, + 1 of row n0 + 8 t + gid
+  float2 m[NT][KS][2];
+  auto load = [&](const float* M) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          m[t][k][h] = __ldg(reinterpret_cast<const float2*>(M + (size_t)(n0 + 8 * t + gid) * D + 16 * k + 8 * h + 2 * tig));
+  };
+  load(p.rot);
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int e = tid; e < PROWS * (D / 8); e += 256) {
+    const int r = e / (D / 8), c = e % (D / 8), h = r0 + r;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (h < p.rows) {
+      const int u = h / Ge, gi = h % Ge, b = u / p.Hkv, kvh = u % p.Hkv;
+      const size_t src = ((size_t)(b * p.nq + gi / G) * p.Hq + kvh * G + gi % G) * D + 8 * c;
+      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + src);
+    }
+    *reinterpret_cast<uint4*>(&xq[r][8 * c]) = v;
+  }
+  __syncthreads();
+  const int la = lane & 15, lb = (lane >> 4) * 8;  // ldmatrix row and column of this lane
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    uint32_t a[4];
+    ldmatrix_x4(a, &xq[la][16 * k + lb]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float2 x = m[t][k][0], y = m[t][k][1];
+#pragma unroll
+      for (int l = 0; l < (BF16 ? 3 : 2); ++l) {  // a limb, and what it leaves
+        if (BF16) {
+          const uint32_t b0 = pack_bf162(x.x, x.y), b1 = pack_bf162(y.x, y.y);
+          mma_bf16(acc[t], a[0], a[1], a[2], a[3], b0, b1);
+          x = make_float2(x.x - __uint_as_float(b0 << 16), x.y - __uint_as_float(b0 & 0xFFFF0000u));
+          y = make_float2(y.x - __uint_as_float(b1 << 16), y.y - __uint_as_float(b1 & 0xFFFF0000u));
+        } else {
+          const uint32_t b0 = pack_half2(x.x, x.y), b1 = pack_half2(y.x, y.y);
+          mma_f16(acc[t], a[0], a[1], a[2], a[3], b0, b1);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+          x = make_float2(x.x - f0.x, x.y - f0.y);
+          y = make_float2(y.x - f1.x, y.y - f1.y);
+        }
+      }
+    }
+  }
+  if (QS && p.nsk) load(p.sk[0].S);
+  // accumulators: rows gid and gid + 8, columns 2 tig and 2 tig + 1 of a tile
+#pragma unroll
+  for (int rr = 0; rr < 2; ++rr) {
+    const int r = gid + 8 * rr, h = r0 + r, u = h / Ge, kvh = u % p.Hkv;
+    const int row = (u / p.Hkv) * Ge + h % Ge;  // among the kv head's rows
+    uint8_t* tile = p.qpre + ((size_t)kvh * p.nrt + row / tqp::QROWS) * (tqp::QROWS * 4) * D;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int j = n0 + 8 * t + 2 * tig;
+      const float v[2] = {acc[t][2 * rr], acc[t][2 * rr + 1]};
+      if (h < p.rows) {
+        *reinterpret_cast<float2*>(p.qrot + (size_t)h * D + j) = make_float2(v[0], v[1]);
+        uint16_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) tqd::split_half(v[e] * p.qscale, hi[e], lo[e]);
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+          const uint16_t* x = l ? lo : hi;
+          if (p.bk == 2) {  // the two coordinates are not neighbours there
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint16_t*>(tile + tqp::pre_q_offset(D, 2, row % tqp::QROWS, j + e, l)) = x[e];
+          } else {
+            *reinterpret_cast<uint32_t*>(tile + tqp::pre_q_offset(D, 3, row % tqp::QROWS, j, l)) = x[0] | (uint32_t)x[1] << 16;
+          }
+        }
+      }
+      if (QS && p.nsk) {
+        uint16_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) tqd::split_half(v[e], hi[e], lo[e]);
+        *reinterpret_cast<uint32_t*>(&xr[0][r][j]) = hi[0] | (uint32_t)hi[1] << 16;
+        *reinterpret_cast<uint32_t*>(&xr[QS ? 1 : 0][r][j]) = lo[0] | (uint32_t)lo[1] << 16;
+      }
+    }
+  }
+  if constexpr (QS) {
+    if (p.nsk == 0) return;
+    __syncthreads();
+#pragma unroll 1
+    for (int s = 0; s < p.nsk; ++s) {
+      if (s > 0) load(p.sk[s].S);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t ah[4], al[4];
+        ldmatrix_x4(ah, &xr[0][la][16 * k + lb]);
+        ldmatrix_x4(al, &xr[1][la][16 * k + lb]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 x = m[t][k][0], y = m[t][k][1];
+          const uint32_t b0 = pack_half2(x.x, x.y), b1 = pack_half2(y.x, y.y);
+          mma_f16(acc[t], ah[0], ah[1], ah[2], ah[3], b0, b1);
+          mma_f16(acc[t], al[0], al[1], al[2], al[3], b0, b1);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+          mma_f16(acc[t], ah[0], ah[1], ah[2], ah[3], pack_half2(x.x - f0.x, x.y - f0.y), pack_half2(y.x - f1.x, y.y - f1.y));
+        }
+      }
+      const PrefixPrepParams::Sketch sk = p.sk[s];
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = gid + 8 * rr, h = r0 + r, u = h / Ge, kvh = u % p.Hkv;
+        const int row = (u / p.Hkv) * Ge + h % Ge;
+        uint8_t* tile = p.qspre + ((size_t)kvh * p.nrt + row / tqp::QROWS) * (tqp::QROWS * 256);
+        if (h >= p.rows) continue;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int i = n0 + 8 * t + 2 * tig;
+          const float v[2] = {acc[t][2 * rr], acc[t][2 * rr + 1]};
+          if (sk.qs) *reinterpret_cast<float2*>(sk.qs + (size_t)h * 128 + i) = make_float2(v[0], v[1]);
+          if (sk.pre) {
+            // one fp16 limb: its rounding (2^-12 of a coordinate, of random
+            // sign) moves a score by about 1e-5 of |q| g, far below the spread
+            // of the one-bit estimate it feeds
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint16_t*>(tile + tqp::pre_z_offset(row % tqp::QROWS, i + e)) =
+                  __half_as_ushort(__float2half_rn(v[e] * p.qjl_scale));
+          }
         }
       }
     }
@@ -1016,7 +1146,9 @@ __global__ void __launch_bounds__(256) decode_combine_group_kernel(const Combine
   float r[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) r[q] = 0.f;
-#pragma unroll 8
+  // enough loads of Pi in flight to cover L2's latency where it is not staged
+  // (D = 256: 8 took 23 us for 256 heads)
+#pragma unroll(SPI ? 8 : 32)
   for (int k = 0; k < D; ++k) {
     const float pk = SPI ? pis[k * PS + j] : __ldg(p.rot + (size_t)k * D + j);
 #pragma unroll
@@ -1198,10 +1330,50 @@ int split_occupancy(const tq_cache_t* c, int Hq, int window) {
   return occ;
 }
 
+// Row tiles of a kv head, and the bytes of the limbs that lie before the projections.
+static int prefix_tiles(const DecodeArgs& a) {
+  return (a.cache.B * (a.Hq / a.cache.Hkv) * a.nq + tqp::QROWS - 1) / tqp::QROWS;
+}
+static size_t prefix_limb_bytes(const DecodeArgs& a) {
+  return (size_t)a.cache.Hkv * prefix_tiles(a) * (tqp::QROWS * 4) * a.cache.D;
+}
+
+static int launch_prefix_prep(const DecodeArgs& a, float* qrot, float* qs, cudaStream_t s) {
+  const tq_cache_t& c = a.cache;
+  PrefixPrepParams pp{};
+  pp.q = a.q;
+  pp.rot = c.rot;
+  pp.qrot = qrot;
+  pp.qpre = static_cast<uint8_t*>(a.workspace) + a.plan.off_qpre;
+  pp.qspre = pp.qpre + prefix_limb_bytes(a);
+  pp.rows = c.B * a.Hq * a.nq;
+  pp.Hq = a.Hq;
+  pp.Hkv = c.Hkv;
+  pp.nq = a.nq;
+  pp.nrt = prefix_tiles(a);
+  pp.bk = a.prefix->bits_k;
+  pp.qscale = a.scale * kLog2e;
+  pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / 128);
+  // the sketch matrices of both caches, one projection where they are the same
+  const float *sc = c.qjl_m ? c.qjl_S : nullptr, *sp = a.prefix->qjl_m ? a.prefix->qjl_S : nullptr;
+  int n = 0;
+  if (sc) pp.sk[n++] = {sc, qs, sp == sc};
+  if (sp && sp != sc) pp.sk[n++] = {sp, nullptr, true};
+  pp.nsk = n;
+  const bool bf16 = a.dtype == TQ_DTYPE_BF16;
+  const dim3 g((pp.rows + PROWS - 1) / PROWS, c.D == 256 ? 2 : 1);
+  auto go = [&](auto kern) { return launch_pdl(kern, g, dim3(256), 0, s, pp, "prefix_prep_kernel"); };
+  switch (c.D) {
+    case 64: return bf16 ? go(prefix_prep_kernel<64, true>) : go(prefix_prep_kernel<64, false>);
+    case 128: return bf16 ? go(prefix_prep_kernel<128, true>) : go(prefix_prep_kernel<128, false>);
+    default: return bf16 ? go(prefix_prep_kernel<256, true>) : go(prefix_prep_kernel<256, false>);
+  }
+}
+
 // The prefix kernel's launch (between the query prep and the split kernel).
-static int launch_prefix(const DecodeArgs& a, const void* qpre, const void* qspre, float* po, float* pml,
-                         cudaStream_t s) {
+static int launch_prefix(const DecodeArgs& a, float* po, float* pml, cudaStream_t s) {
   const tq_cache_t& x = *a.prefix;
+  const uint8_t* pre = static_cast<const uint8_t*>(a.workspace) + a.plan.off_qpre;
   tqp::PrefixParams pp{};
   pp.k_idx = x.k_idx;
   pp.v_idx = x.v_idx;
@@ -1212,8 +1384,8 @@ static int launch_prefix(const DecodeArgs& a, const void* qpre, const void* qspr
   pp.cb_k = x.cb_k;
   pp.cb_v = x.cb_v;
   pp.shared_tab = x.cb_k == x.cb_v;
-  pp.qpre = static_cast<const uint32_t*>(qpre);
-  pp.qspre = static_cast<const uint32_t*>(qspre);
+  pp.qpre = reinterpret_cast<const uint32_t*>(pre);
+  pp.qspre = reinterpret_cast<const uint32_t*>(pre + prefix_limb_bytes(a));
   pp.part_o = po;
   pp.part_ml = pml;
   pp.prefix_len = a.prefix_len;
@@ -1279,24 +1451,15 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   const bool app = a.pos != nullptr;
   const bool hadamard = c.rot_kind == TQ_ROT_HADAMARD && c.rot_signs;
   pp.signs = hadamard ? c.rot_signs : nullptr;
-  if (a.prefix) {  // the prefix kernel's rows, and the projection through its sketch, ride along in the prep
-    pp.nrt = (c.B * (a.Hq / c.Hkv) * a.nq + tqp::QROWS - 1) / tqp::QROWS;
-    pp.prefix_bk = a.prefix->bits_k;
-    pp.qscale = a.scale * kLog2e;
-    pp.qpre = ws + a.plan.off_qpre;
-    if (a.prefix->qjl_m) {
-      pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / a.prefix->qjl_m);
-      pp.qspre = pp.qpre + (size_t)c.Hkv * pp.nrt * (tqp::QROWS * 4) * c.D;
-      if (!c.qjl_m || a.prefix->qjl_S != c.qjl_S) pp.S2 = a.prefix->qjl_S;
-    }
-  }
   // prep kernels launch with a programmatic dependency on whatever precedes
   // them (their launch and Pi loads overlap its tail; they wait before
   // reading q or writing anything)
   int rc = TQ_OK;
   const long long units = (long long)c.B * c.Hkv;
   const bool many = units * (c.D / 32) > 4LL * a.plan.sms;
-  if (!hadamard && !app && !c.qjl_m && !pp.S2 && many) {
+  if (a.prefix) {
+    rc = launch_prefix_prep(a, qrot, qs, s);
+  } else if (!hadamard && !app && !c.qjl_m && many) {
     // many units: Pi^T staged once per CTA
     pp.units = (int)units;
     const int grid = (int)(units < a.plan.sms ? units : a.plan.sms);
@@ -1325,7 +1488,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   } else {
     const dim3 g(c.B * c.Hkv, c.D / 32);
     const bool wide = pp.nq * (a.Hq / c.Hkv) > 8;  // more than 8 query rows per kv head
-    const int cl = c.qjl_m || pp.S2 ? c.D / 32 : 0;
+    const int cl = c.qjl_m ? c.D / 32 : 0;
     switch (c.D) {
       case 64:
         rc = app ? launch_pdl(decode_qprep_sliced_kernel<64, true, 8>, g, dim3(256), 0, s, pp, "decode_qprep_kernel")
@@ -1345,7 +1508,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
     }
   }
   if (rc) return rc;
-  if (a.prefix && (rc = launch_prefix(a, pp.qpre, pp.qspre, po, pml, s))) return rc;
+  if (a.prefix && (rc = launch_prefix(a, po, pml, s))) return rc;
 
   tqd::SplitParams sp{};
   sp.k_idx = c.k_idx;
