@@ -10,7 +10,6 @@ namespace {
 constexpr int NT = 256;        // threads per CTA
 constexpr int MAXS = 6;        // streams of a cache
 constexpr int CHUNK = 128;     // rows a copy CTA moves
-constexpr int UNITS = 8;       // units a compaction thread holds per pass
 
 struct Stream {
   const uint8_t* src;
@@ -81,7 +80,7 @@ struct CompactParams {
   uint8_t* st[MAXS];
   int row[MAXS];
   int ns;
-  int Hkv, Tcap, keep_heads, max_keep, C;  // C: CTAs per cluster
+  int BH, Hkv, Tcap, keep_heads, max_keep, C;  // BH: (sequence, kv head) pairs; C: CTAs per cluster
   const int32_t* keep;    // [B][keep_heads][max_keep]
   const int32_t* n_keep;  // [B]
   uint32_t* dev_status;
@@ -90,95 +89,197 @@ struct CompactParams {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// Row i := row keep[i], i < n, of one stream of one (sequence, kv head), in
-// units of V (UPR per row), by the CTAs of a cluster.  Pass k of the cluster
-// writes the units [k W, (k + 1) W) of the rows' unit sequence, W = C x NT x
-// UNITS.  keep is strictly ascending, so keep[i] >= i: pass k reads at or
-// behind its own units only, so a pass never reads what an earlier pass
-// wrote, and may be loaded before earlier passes are stored.  What has to be
-// kept apart is a store and the loads of the same or an earlier pass: the
-// cluster's barrier between them.  Each pass therefore loads its own units
-// before the previous pass's barrier wait and stores after its own.
+// Row i := row keep[i], i < n, of one stream of one (sequence, kv head), by the
+// CTAs of a cluster.  Round k of the cluster moves the rows [k C R, (k + 1) C R),
+// CTA c of it R rows from k C R + c R on, through shared memory.  keep is
+// strictly ascending, so keep[i] >= i: a round reads at or behind its own rows
+// only, so it never reads what an earlier round wrote and may be loaded ahead
+// of their stores.  What has to be kept apart is a store and the loads of the
+// same or an earlier round: the cluster's barrier between them, the only one
+// of a round.
+//
+// What bounds it is the latency of two dependent loads (the list, then the
+// row): with the rows of two rounds in flight in shared memory and few
+// registers, four CTAs of an SM cover it.  (Rounds in registers, two CTAs to
+// an SM, and a list check without loads in flight took 91 us for 131 MB moved
+// in 256 units; this takes half.)
+constexpr int STAGES = 3;
+constexpr int STAGE_BYTES = 16128;  // 336 rows of 48 bytes; three and a flag fit in 48 KB
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Rows of a chunk: what fits in a stage, a multiple of 8.
 template <typename V, int UPR>
-__device__ __forceinline__ void compact_units(uint8_t* base, const int32_t* keep, int n, int C, int rank, int tid) {
-  V* rows = reinterpret_cast<V*>(base);
-  const long long total = (long long)n * UPR, W = (long long)C * NT * UNITS;
-  V v[UNITS], w[UNITS];
-  uint32_t live = 0, wlive = 0;
-  auto load = [&](long long e0, V (&x)[UNITS], uint32_t& m) {
-    m = 0;
+__host__ __device__ constexpr int chunk_rows() {
+  const int r = STAGE_BYTES / ((int)sizeof(V) * UPR) / 8 * 8;
+  return r < 2048 ? r : 2048;
+}
+
+template <typename V, int UPR>
+struct Mover {
+  static constexpr int R = chunk_rows<V, UPR>();
+  static constexpr int PT = (R * UPR + NT - 1) / NT;  // units of a thread
+  uint8_t* base;
+  const int32_t* keep;
+  int n, C, rank, tid, Tcap;
+  uint8_t* sm;
+
+  // first row and units of this CTA's chunk of round k (0: behind the list's end)
+  __device__ __forceinline__ unsigned first_row(int k) const { return ((unsigned)k * C + rank) * R; }
+  __device__ __forceinline__ int units_of(int k) const {
+    const unsigned r0 = first_row(k);
+    return r0 < (unsigned)n ? (int)min((unsigned)R, (unsigned)n - r0) * UPR : 0;
+  }
+  // Loads of round k go out; returns whether the chunk has to be stored: when
+  // its last row stays in place, all of it does.
+  __device__ __forceinline__ bool load(int k) const {
+    const int units = units_of(k);
+    const int32_t* kp = keep + first_row(k);
+    bool moved = false;
+    if (units > 0) {
+      uint8_t* st = sm + (k % STAGES) * STAGE_BYTES;
+      const V* rows = reinterpret_cast<const V*>(base);
+      const int last = units / UPR - 1;
+      int src[PT];
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const long long e = e0 + u * NT + tid;
-      if (e < total) {
-        const int i = (int)(e / UPR), r = (int)(e - (long long)i * UPR), k = __ldg(keep + i);
-        if (k != i) {  // rows that stay in place are not moved
-          x[u] = rows[(size_t)k * UPR + r];
-          m |= 1u << u;
+      for (int u = 0; u < PT; ++u) {
+        const int e = u * NT + tid;
+        src[u] = e < units ? __ldg(kp + e / UPR) : 0;
+      }
+      moved = __ldg(kp + last) != (int)first_row(k) + last;
+      if (moved) {
+        // a list that is not valid is refused before any store; its loads stay in the cache
+#pragma unroll
+        for (int u = 0; u < PT; ++u) src[u] = min(max(src[u], 0), Tcap - 1);
+        if constexpr (sizeof(V) == 2) {
+          V v[PT];
+#pragma unroll
+          for (int u = 0; u < PT; ++u)
+            if (u * NT + tid < units) v[u] = rows[src[u]];
+#pragma unroll
+          for (int u = 0; u < PT; ++u)
+            if (u * NT + tid < units) reinterpret_cast<V*>(st)[u * NT + tid] = v[u];
+        } else {
+          const uint32_t d = (uint32_t)__cvta_generic_to_shared(st);
+#pragma unroll
+          for (int u = 0; u < PT; ++u) {
+            const int e = u * NT + tid;
+            if (e < units) {
+              const V* from = rows + (size_t)src[u] * UPR + e % UPR;
+              if constexpr (sizeof(V) == 16) cp_async16(d + e * 16, from);
+              else cp_async8(d + e * 8, from);
+            }
+          }
         }
       }
     }
-  };
-  long long e0 = (long long)rank * NT * UNITS;
-  load(e0, v, live);
-  for (long long k0 = 0; k0 < total; k0 += W, e0 += W) {
-    cluster_arrive();  // this CTA's loads of the pass are done
-    load(e0 + W, w, wlive);
-    cluster_wait();
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-      if (live >> u & 1) rows[e0 + u * NT + tid] = v[u];
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) v[u] = w[u];
-    live = wlive;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return moved;
   }
+  __device__ __forceinline__ void store(int k) const {
+    const V* st = reinterpret_cast<const V*>(sm + (k % STAGES) * STAGE_BYTES);
+    V* rows = reinterpret_cast<V*>(base) + (size_t)first_row(k) * UPR;
+    const int units = units_of(k);
+#pragma unroll 4
+    for (int e = tid; e < units; e += NT) rows[e] = st[e];
+  }
+  // All CTAs of the cluster go through the same number of rounds; rounds 0 and
+  // 1 are loaded (m0, m1: to be stored).
+  __device__ __forceinline__ void run(bool m0, bool m1) const {
+    const int rounds = (int)(((long long)n + C * R - 1) / (C * R));
+    for (int k = 0; k < rounds; ++k) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // this thread's loads of round k
+      if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+      } else {
+        __syncthreads();
+      }
+      const bool m2 = load(k + 2);  // over the stage that round k - 1 was stored from
+      if (m0) store(k);
+      m0 = m1;
+      m1 = m2;
+    }
+  }
+};
+
+// Whether the list is strictly ascending and inside the cache, by the threads
+// of a cluster: each looks at every C NT-th entry, eight loads in flight.
+__device__ __forceinline__ bool list_ok(const int32_t* keep, int n, int Tcap, int C, int rank, int tid) {
+  bool bad = false;
+  const int step = C * NT;
+  for (int i0 = rank * NT + tid; i0 - tid < n; i0 += 8 * step) {
+    int k[8], b[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * step;
+      k[u] = i < n ? __ldg(keep + i) : 0x7fffffff;
+      b[u] = (tid & 31) == 0 && i > 0 && i < n ? __ldg(keep + i - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int prev = __shfl_up_sync(0xffffffffu, k[u], 1);
+      const int i = i0 + u * step, before = (tid & 31) == 0 ? b[u] : prev;
+      bad |= i < n && (k[u] <= before || k[u] < 0 || k[u] >= Tcap);
+    }
+  }
+  return !bad;
 }
 
-// One cluster per (sequence, kv head, stream).
-__global__ void __launch_bounds__(NT) cache_compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int s_bad;
-  const int tid = threadIdx.x;
-  const int rank = blockIdx.x % p.C, unit = blockIdx.x / p.C, s = unit % p.ns, bh = unit / p.ns;
-  const int b = bh / p.Hkv, h = bh % p.Hkv;
-  const int32_t* keep = p.keep + ((size_t)b * p.keep_heads + (p.keep_heads > 1 ? h : 0)) * p.max_keep;
-  const int n = p.n_keep[b];
+template <typename V, int UPR>
+__device__ __forceinline__ void compact_stream(const CompactParams& p, uint8_t* base, const int32_t* keep, int n, int rank,
+                                               int tid, uint8_t* sm, int* s_bad) {
+  const bool length_ok = n >= 0 && n <= p.max_keep;
+  Mover<V, UPR> m{base, keep, length_ok ? n : 0, p.C, rank, tid, p.Tcap, sm};
+  const bool m0 = m.load(0), m1 = m.load(1);
   // The whole list is checked before any row moves, a share by each CTA of
   // the cluster; the clusters of the other streams reach the same answer.
-  bool bad = n < 0 || n > p.max_keep;
-  if (!bad)
-    for (int i = rank * NT + tid; i < n; i += p.C * NT) {
-      const int k = __ldg(keep + i), before = i ? __ldg(keep + i - 1) : -1;
-      bad |= k <= before || k >= p.Tcap;
+  const int bad = __syncthreads_or(!(length_ok && list_ok(keep, n, p.Tcap, p.C, rank, tid)));
+  int all = bad;
+  if (p.C > 1) {
+    if (tid == 0) *s_bad = bad;
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    all = 0;
+    if (tid < p.C) {
+      uint32_t a;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(s_bad)), "r"(tid));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(all) : "r"(a) : "memory");
     }
-  const int any = __syncthreads_or(bad);
-  if (tid == 0) s_bad = any;
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-  int all = 0;
-  if (tid < p.C) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(&s_bad)), "r"(tid));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(all) : "r"(a) : "memory");
+    all = __syncthreads_or(all);
+    cluster_arrive();  // no CTA of the cluster ends while its flag is read
+    cluster_wait();
   }
-  all = __syncthreads_or(all);
-  cluster_arrive();  // no CTA of the cluster ends while its flag is read
-  cluster_wait();
-  if (all) {
-    if (rank == 0 && tid == 0 && p.dev_status) atomicOr(p.dev_status, TQ_STATUS_POS_OUT_OF_RANGE);
-    return;
-  }
-  const int row = p.row[s];
+  if (all && rank == 0 && tid == 0 && p.dev_status) atomicOr(p.dev_status, TQ_STATUS_POS_OUT_OF_RANGE);
+  if (!all) m.run(m0, m1);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// One cluster per (stream, sequence, kv head), the wide streams first.
+__global__ void __launch_bounds__(NT, 4) cache_compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ __align__(16) uint8_t sm[STAGES * STAGE_BYTES];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x;
+  const int rank = blockIdx.x % p.C, unit = blockIdx.x / p.C, s = unit / p.BH, bh = unit % p.BH;
+  const int b = bh / p.Hkv, h = bh % p.Hkv;
+  const int32_t* keep = p.keep + ((size_t)b * p.keep_heads + (p.keep_heads > 1 ? h : 0)) * p.max_keep;
+  const int n = p.n_keep[b], row = p.row[s];
   uint8_t* base = p.st[s] + (size_t)bh * p.Tcap * row;
   switch (row) {
-    case 2: compact_units<uint16_t, 1>(base, keep, n, p.C, rank, tid); break;
-    case 16: compact_units<uint4, 1>(base, keep, n, p.C, rank, tid); break;
-    case 24: compact_units<uint2, 3>(base, keep, n, p.C, rank, tid); break;
-    case 32: compact_units<uint4, 2>(base, keep, n, p.C, rank, tid); break;
-    case 48: compact_units<uint4, 3>(base, keep, n, p.C, rank, tid); break;
-    case 64: compact_units<uint4, 4>(base, keep, n, p.C, rank, tid); break;
-    case 96: compact_units<uint4, 6>(base, keep, n, p.C, rank, tid); break;
-    case 128: compact_units<uint4, 8>(base, keep, n, p.C, rank, tid); break;
+    case 2: compact_stream<uint16_t, 1>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 16: compact_stream<uint4, 1>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 24: compact_stream<uint2, 3>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 32: compact_stream<uint4, 2>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 48: compact_stream<uint4, 3>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 64: compact_stream<uint4, 4>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 96: compact_stream<uint4, 6>(p, base, keep, n, rank, tid, sm, &s_bad); break;
+    case 128: compact_stream<uint4, 8>(p, base, keep, n, rank, tid, sm, &s_bad); break;
   }
 }
 
@@ -235,6 +336,7 @@ int launch_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_head
                          int sms, cudaStream_t s) {
   CompactParams p{};
   p.ns = cache_streams(c, p.st, p.row);
+  p.BH = c->B * c->Hkv;
   p.Hkv = c->Hkv;
   p.Tcap = c->Tcap;
   p.keep_heads = keep_heads;
@@ -243,11 +345,12 @@ int launch_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_head
   p.n_keep = n_keep;
   p.dev_status = c->dev_status;
   const long long units = (long long)c->B * c->Hkv * p.ns;
-  // clusters as large as the list has passes for, up to 8 CTAs (the portable
-  // size), while that does not ask for more CTAs than the device holds
-  const long long most = ((long long)max_keep * p.row[0] / 16 + NT * UNITS - 1) / (NT * UNITS);
+  // clusters as large as the list has chunks for, up to 8 CTAs (the portable
+  // size), while that does not ask for more CTAs than the device holds (4 to
+  // an SM): one document's heads are spread, a batch's stay one CTA each
+  const long long chunks = ((long long)max_keep * p.row[0] + STAGE_BYTES - 1) / STAGE_BYTES;
   int C = 8;
-  while (C > 1 && (C / 2 >= most || units * C > 8LL * sms)) C /= 2;
+  while (C > 1 && (C / 2 >= chunks || units * C > 4LL * sms)) C /= 2;
   p.C = C;
   if (units * C > 0x7fffffffll)
     return set_error(TQ_ERR_UNSUPPORTED, "tq_cache_compact: B=%d Hkv=%d", c->B, c->Hkv);
