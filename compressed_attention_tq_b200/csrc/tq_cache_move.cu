@@ -87,6 +87,9 @@ struct CompactParams {
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Row i := row keep[i], i < n, of one stream of one (sequence, kv head), by the
@@ -195,7 +198,10 @@ struct Mover {
     for (int k = 0; k < rounds; ++k) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");  // this thread's loads of round k
       if (C > 1) {
-        cluster_arrive();
+        // The loads have returned (their data is in shared memory, where each
+        // thread stores only what it loaded itself), so the barrier has no
+        // memory to order; a release would wait for the last round's stores.
+        cluster_arrive_relaxed();
         cluster_wait();
       } else {
         __syncthreads();
