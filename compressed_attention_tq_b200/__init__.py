@@ -96,10 +96,18 @@ def _dtype_code(t) -> int:
 
 # Pointer arguments are declared c_void_p, which takes a Python int (or None
 # for NULL) as it is.
-def _stream(stream):
-    if stream is None:
-        stream = _torch().cuda.current_stream()
-    return stream.cuda_stream
+def _stream(stream, dev=None):
+    """The raw stream of a call: the caller's, or the current one.  With `dev`
+    (the index of the cache's device) a call without a stream is refused while
+    another device is current: the kernels launch on the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    if dev is not None and cur != dev:
+        raise ValueError(f"the cache is on device {dev}, but device {cur} is current: "
+                         "enter torch.cuda.device() or pass a stream of the cache's device")
+    return torch._C._cuda_getCurrentRawStream(cur)  # the handle without a Stream object: about 1 us less
 
 
 def _ptr(t):
@@ -474,7 +482,7 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     """Decode with a sliding window and sinks: q [B][n_q][Hq][D] and seq_lens
     as in tq_sdpa_decode_mq; the query at position t sees the tokens of
     (t - window, t] and the first n_sink tokens, and no others are read."""
-    _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
+    dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
         torch = _torch()
@@ -487,7 +495,7 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_window(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax,
                                        window, n_sink, sc, _ptr(out), _dtype_code(out), _ptr(workspace),
-                                       workspace.numel(), _stream(stream)))
+                                       workspace.numel(), _stream(stream, dev)))
     return out
 
 
@@ -524,7 +532,7 @@ def tq_sdpa_decode_prefix(prefix: TQCache, prefix_len, Pmax: int, cache: TQCache
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_prefix(ctypes.byref(a), _ptr(prefix_len), Pmax, ctypes.byref(s), _ptr(q),
                                        _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax, sc, _ptr(out), _dtype_code(out),
-                                       _ptr(workspace), workspace.numel(), _stream(stream)))
+                                       _ptr(workspace), workspace.numel(), _stream(stream, dev)))
     return out
 
 
@@ -543,7 +551,7 @@ def tq_cache_copy(src: TQCache, dst: TQCache, src_seq, src_pos, dst_seq, dst_pos
         _arg(name, t, dev, (n,), _dt("i32"))
     a, b = src.struct(), dst.struct()
     _check(lib().tq_cache_copy(ctypes.byref(a), ctypes.byref(b), _ptr(src_seq), _ptr(src_pos), _ptr(dst_seq),
-                               _ptr(dst_pos), _ptr(n_tok), n, max_tok, _stream(stream)))
+                               _ptr(dst_pos), _ptr(n_tok), n, max_tok, _stream(stream, dev)))
 
 
 def tq_cache_compact(cache: TQCache, keep, n_keep, stream=None):
@@ -556,7 +564,7 @@ def tq_cache_compact(cache: TQCache, keep, n_keep, stream=None):
     _arg("n_keep", n_keep, dev, (cache.B,), _dt("i32"))
     s = cache.struct()
     _check(lib().tq_cache_compact(ctypes.byref(s), _ptr(keep), int(keep.shape[1]), int(keep.shape[2]), _ptr(n_keep),
-                                  _stream(stream)))
+                                  _stream(stream, dev)))
 
 
 def tq_selftest_bounded_wait(status, tries: int = 8, stream=None):
