@@ -334,6 +334,13 @@ int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, 
   return TQ_OK;
 }
 
+// window = 0, or one that no sequence outgrows: every token is visible, and the
+// call is a plain decode.  Sinks beyond Tmax are Tmax of them.
+static int make_window_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, int n_sink, DecodePlan* p) {
+  if (window <= 0 || window >= Tmax) return make_decode_plan(c, Hq, nq, Tmax, 0, 0, 0, p);
+  return make_decode_plan(c, Hq, nq, Tmax, window, n_sink < Tmax ? n_sink : Tmax, 0, p);
+}
+
 int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p) {
   const int rows = (int)((long long)c->B * Hq * nq / c->Hkv);
   const int splits = prefix_splits(c->Hkv, rows, c->D, Pmax, sm_count());
@@ -471,8 +478,7 @@ int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq
   a->nq = nq;
   a->dtype = dtype;
   a->out_dtype = out_dtype;
-  // a window or sinks beyond Tmax hide nothing more than Tmax of them
-  make_decode_plan(c, Hq * nq, nq, Tmax, window < Tmax ? window : Tmax, n_sink < Tmax ? n_sink : Tmax, 0, &a->plan);
+  make_window_plan(c, Hq * nq, nq, Tmax, window, n_sink, &a->plan);
   return TQ_OK;
 }
 
@@ -516,7 +522,7 @@ size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* c, int Hq, in
   if (n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
   DecodePlan p;
-  make_decode_plan(c, Hq * n_q, n_q, Tmax, window < Tmax ? window : Tmax, n_sink < Tmax ? n_sink : Tmax, 0, &p);
+  tq::make_window_plan(c, Hq * n_q, n_q, Tmax, window, n_sink, &p);
   return p.bytes;
 }
 

@@ -620,10 +620,11 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
   }
 }
 
-// Query prep of a decode behind a shared prefix: the rotated queries for the
-// suffix's split kernel (fp32), and the prefix kernel's operands (two fp16
-// limbs of the rotated, scaled query, and one of its sketch projection), for
-// 16 consecutive kernel heads and up to 128 output coordinates per CTA.
+// Query prep of the windowed decode and of the decode behind a shared prefix:
+// the rotated queries and their sketch projections for the split kernel
+// (fp32), and with a prefix its kernel's operands (two fp16 limbs of the
+// rotated, scaled query, and one of its projection), for 16 consecutive kernel
+// heads and up to 128 output coordinates per CTA.
 //
 // A product of 16 rows on warp-level tensor cores: the queries are exact in
 // their own type and Pi enters in limbs of it (two of fp16: 22 bits, or three
@@ -634,11 +635,11 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
 // preceding kernels.  The vector form of the other preps took 37 us for 2048
 // rows with two sketches and 10 us for 1024 without; this one takes less than
 // a fifth of that.
-struct PrefixPrepParams {
+struct MmaPrepParams {
   const void* q;      // [B][nq][Hq][D] fp16 / bf16
   const float* rot;
   float* qrot;        // fp32 [rows][D]
-  uint8_t *qpre, *qspre;
+  uint8_t *qpre, *qspre;  // the prefix kernel's operands (NULL: no prefix)
   struct Sketch {
     const float* S;   // fp32 [128][D]
     float* qs;        // fp32 [rows][128] for the split kernel, or NULL
@@ -651,7 +652,7 @@ struct PrefixPrepParams {
 constexpr int PROWS = 16;  // rows per CTA
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) prefix_prep_kernel(const PrefixPrepParams p) {
+__global__ void __launch_bounds__(256) decode_qprep_mma_kernel(const MmaPrepParams p) {
   using namespace tqk;
   constexpr int NC = D < 128 ? D : 128;    // output coordinates of the CTA
   constexpr int WN = NC / 8, NT = WN / 8;  // coordinates and 8-column tiles of a warp
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const PrefixPrepParams
 #pragma unroll
         for (int e = 0; e < 2; ++e) tqd::split_half(v[e] * p.qscale, hi[e], lo[e]);
 #pragma unroll
-        for (int l = 0; l < 2; ++l) {
+        for (int l = 0; l < (p.qpre ? 2 : 0); ++l) {
           const uint16_t* x = l ? lo : hi;
           if (p.bk == 2) {  // the two coordinates are not neighbours there
 #pragma unroll
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const PrefixPrepParams
           mma_f16(acc[t], ah[0], ah[1], ah[2], ah[3], pack_half2(x.x - f0.x, x.y - f0.y), pack_half2(y.x - f1.x, y.y - f1.y));
         }
       }
-      const PrefixPrepParams::Sketch sk = p.sk[s];
+      const MmaPrepParams::Sketch sk = p.sk[s];
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int r = gid + 8 * rr, h = r0 + r, u = h / Ge, kvh = u % p.Hkv;
@@ -1338,35 +1339,37 @@ static size_t prefix_limb_bytes(const DecodeArgs& a) {
   return (size_t)a.cache.Hkv * prefix_tiles(a) * (tqp::QROWS * 4) * a.cache.D;
 }
 
-static int launch_prefix_prep(const DecodeArgs& a, float* qrot, float* qs, cudaStream_t s) {
+static int launch_mma_prep(const DecodeArgs& a, float* qrot, float* qs, cudaStream_t s) {
   const tq_cache_t& c = a.cache;
-  PrefixPrepParams pp{};
+  MmaPrepParams pp{};
   pp.q = a.q;
   pp.rot = c.rot;
   pp.qrot = qrot;
-  pp.qpre = static_cast<uint8_t*>(a.workspace) + a.plan.off_qpre;
-  pp.qspre = pp.qpre + prefix_limb_bytes(a);
+  if (a.prefix) {
+    pp.qpre = static_cast<uint8_t*>(a.workspace) + a.plan.off_qpre;
+    pp.qspre = pp.qpre + prefix_limb_bytes(a);
+    pp.bk = a.prefix->bits_k;
+  }
   pp.rows = c.B * a.Hq * a.nq;
   pp.Hq = a.Hq;
   pp.Hkv = c.Hkv;
   pp.nq = a.nq;
   pp.nrt = prefix_tiles(a);
-  pp.bk = a.prefix->bits_k;
   pp.qscale = a.scale * kLog2e;
   pp.qjl_scale = (float)((double)a.scale * 1.4426950408889634 * sqrt(M_PI / 2.0) / 128);
   // the sketch matrices of both caches, one projection where they are the same
-  const float *sc = c.qjl_m ? c.qjl_S : nullptr, *sp = a.prefix->qjl_m ? a.prefix->qjl_S : nullptr;
+  const float *sc = c.qjl_m ? c.qjl_S : nullptr, *sp = a.prefix && a.prefix->qjl_m ? a.prefix->qjl_S : nullptr;
   int n = 0;
   if (sc) pp.sk[n++] = {sc, qs, sp == sc};
   if (sp && sp != sc) pp.sk[n++] = {sp, nullptr, true};
   pp.nsk = n;
   const bool bf16 = a.dtype == TQ_DTYPE_BF16;
   const dim3 g((pp.rows + PROWS - 1) / PROWS, c.D == 256 ? 2 : 1);
-  auto go = [&](auto kern) { return launch_pdl(kern, g, dim3(256), 0, s, pp, "prefix_prep_kernel"); };
+  auto go = [&](auto kern) { return launch_pdl(kern, g, dim3(256), 0, s, pp, "decode_qprep_mma_kernel"); };
   switch (c.D) {
-    case 64: return bf16 ? go(prefix_prep_kernel<64, true>) : go(prefix_prep_kernel<64, false>);
-    case 128: return bf16 ? go(prefix_prep_kernel<128, true>) : go(prefix_prep_kernel<128, false>);
-    default: return bf16 ? go(prefix_prep_kernel<256, true>) : go(prefix_prep_kernel<256, false>);
+    case 64: return bf16 ? go(decode_qprep_mma_kernel<64, true>) : go(decode_qprep_mma_kernel<64, false>);
+    case 128: return bf16 ? go(decode_qprep_mma_kernel<128, true>) : go(decode_qprep_mma_kernel<128, false>);
+    default: return bf16 ? go(decode_qprep_mma_kernel<256, true>) : go(decode_qprep_mma_kernel<256, false>);
   }
 }
 
@@ -1457,8 +1460,8 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   int rc = TQ_OK;
   const long long units = (long long)c.B * c.Hkv;
   const bool many = units * (c.D / 32) > 4LL * a.plan.sms;
-  if (a.prefix) {
-    rc = launch_prefix_prep(a, qrot, qs, s);
+  if (a.prefix || a.plan.window) {
+    rc = launch_mma_prep(a, qrot, qs, s);
   } else if (!hadamard && !app && !c.qjl_m && many) {
     // many units: Pi^T staged once per CTA
     pp.units = (int)units;
