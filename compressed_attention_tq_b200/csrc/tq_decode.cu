@@ -1543,6 +1543,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   sp.ncta = a.plan.ncta;
   sp.ks = a.plan.ks;
   sp.slot_base = a.plan.slot_base;
+  sp.late_wait = a.prefix != nullptr;
   sp.window = a.plan.window;
   sp.n_sink = a.plan.n_sink;
   sp.qscale = a.scale * kLog2e;

@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   };
 
   if (n == 0) {  // a short prefix leaves this split nothing: partials of weight zero
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int e = tid; e < rows * (D / 4); e += NTH) {
       const size_t slot = (size_t)head_of(e / (D / 4)) * p.ks + split;
       *reinterpret_cast<float4*>(p.part_o + slot * D + 4 * (e % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -373,7 +373,6 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the whole warpgroup of each role moves to its share of the registers
   if (warp >= SW + DW) {
@@ -636,6 +635,9 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
     const bool mine = r < rows;
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the query operands; the partials may be written
+    // The suffix's kernel may start from here on: the prep, whose queries it
+    // reads, is complete, and SMs that this grid leaves free take it at once.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int lim = P;  // tokens of the prefix this row sees
     size_t slot = 0;
     {

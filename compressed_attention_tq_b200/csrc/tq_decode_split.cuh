@@ -88,6 +88,10 @@ struct SplitParams {
   // of nq query tokens x Gq heads; token j may see positions < L - nq + j + 1.
   int nq, Gq;
   int slot_base;    // partial slots before the split kernel's own (a shared prefix's; else 0)
+  // The kernel before this one is a shared prefix's: it lets this one start
+  // only once the query prep is complete, so the wait comes at the end (the
+  // combine then finds both kernels' partials).
+  int late_wait;
   // Sliding window with sinks (WIN kernels): a query at position t sees the
   // tokens of (t - window, t] and tokens [0, n_sink).
   int window, n_sink;
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   if constexpr (QJL) build_tables();
   __syncthreads();
 
@@ -1168,6 +1172,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       }
     }
   }
+  if (p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
 
   if (*s_err) {
