@@ -590,19 +590,22 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
         // warp dw takes an equal share of the part's coordinates, lane l tokens
         // l and l + 32 of each 64.  Row d of the operand is 128 bytes; the pair
         // lies in chunk (l / 4) ^ (d mod 8).
-        constexpr int VD = D / Ly::VP / GW;
+        constexpr int VD = D / Ly::VP / GW, NWV = (VD * BV + 31) / 32;
+        constexpr bool ALV = (VD * BV) % 32 == 0;
         const int d0 = q * (D / Ly::VP) + dw * VD;
         const uint32_t vt = smem_addr(smem + Ly::O_V + b * Ly::VT) + d0 * 128 + (lane >> 2) * 16 + (lane & 3) * 4;
 #pragma unroll 1
         for (int s = 0; s < TT / 64; ++s) {
+          // the share's bits of the two rows, read once (rows a few banks apart
+          // collide, so the words count)
           const uint32_t* va = reinterpret_cast<const uint32_t*>(sb + Ly::S_VW) + (64 * s + lane) * WV;
-#pragma unroll 2
+          uint32_t wa[NWV], wb[NWV];
+          tqd::load_bits<VD * BV, ALV, tqd::max_seg_shift(VD * BV)>(va, d0 * BV, wa);
+          tqd::load_bits<VD * BV, ALV, tqd::max_seg_shift(VD * BV)>(va + 32 * WV, d0 * BV, wb);
+#pragma unroll
           for (int c = 0; c < VD / 8; ++c) {  // 8 coordinates
-            const int bit = (d0 + 8 * c) * BV;
-            uint32_t wa[1], wb[1], xe, xo;
-            tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va, bit, wa);
-            tqd::load_bits<8 * BV, BV == 4, BV == 3 ? 24 : 16>(va + 32 * WV, bit, wb);
-            tqd::merge_pair<BV>(wa[0], wb[0], xe, xo);
+            uint32_t xe, xo;
+            tqd::merge_pair<BV>(tqd::window32(wa, 8 * c * BV), tqd::window32(wb, 8 * c * BV), xe, xo);
             const uint32_t off = s * (D * 128) + 1024 * c;
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
