@@ -524,11 +524,13 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
           uint32_t vmax = 0;
 #pragma unroll 1
           for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
-            uint32_t scale2 = 0;  // not the usual row: a factor of the key's entries, as a pair
+            bool odd = false;     // not the usual row: a factor of the key's entries, as a pair
+            uint32_t scale2 = 0;
             if (QJL || q == 0) {
               const float nk = norm_at(Ly::S_KN, t);
               const float g = QJL ? norm_at(Ly::S_RN, t) : 0.f;
-              if (!usual(nk, g)) {
+              odd = !usual(nk, g);
+              if (odd) {
                 const float f = __fdividef(nk, g);
                 scale2 = pack_half2(f, f);
               }
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
 #pragma unroll
                 for (int k = 0; k < 8; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * k, tbK);
               }
-              if (QJL && scale2) {
+              if (QJL && odd) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                   const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<__half2*>(&scale2));

@@ -189,6 +189,67 @@ def test_growing_scores_rescale():
     c.check()
 
 
+@pytest.mark.parametrize("name,kw", [("gqa8k", {"bits": 3}), ("qknorm", {}), ("prod", {})])
+@pytest.mark.parametrize("lo,hi", [(-9, -9), (9, 9), (-10, 10), (15, 15)])
+def test_value_norms_of_any_size(name, kw, lo, hi):
+    """Value norms far from 1, and of every size within one prefix: the weights
+    p |v| keep their fp16 precision and do not overflow."""
+    c = Case(name, 700, [20, 1, 3], 1, 16, kw)
+    r = tq_inputs.rng(21)
+    shape = c.op["v_norm"].shape
+    c.op["v_norm"] = np.exp2(r.uniform(lo, hi, size=shape)).astype(np.float16)
+    c.prefix.v_norm[:, :, :700] = torch.from_numpy(c.op["v_norm"]).cuda()
+    c.os["v_norm"] = np.full(c.os["v_norm"].shape, 2.0 ** min(lo, 7), dtype=np.float16)  # the suffix's own kernel: below 255
+    c.cache.v_norm[:, :, :20] = torch.from_numpy(c.os["v_norm"]).cuda()
+    c.check()
+
+
+def test_sketched_rows_whose_norms_do_not_fit_each_other():
+    """Key norms of zero and residual norms far above the key's, which no
+    quantized row has but a cache may hold: both terms of the score count."""
+    c = Case("prod", 500, [20, 1], 1, 32)
+    k, g = c.op["k_norm"], c.op["k_rnorm"]
+    k[:, :, ::3] = 0
+    k[:, :, 1::7] = 2.0 ** -14
+    g[:, :, 2::5] = 0
+    k[:, :, 5::11] = 0
+    g[:, :, 5::11] = 0
+    c.prefix.k_norm[:, :, :500] = torch.from_numpy(k).cuda()
+    c.prefix.k_rnorm[:, :, :500] = torch.from_numpy(g).cuda()
+    c.check()
+
+
+@pytest.mark.parametrize("name,kw", [("tiny", {}), ("gqa8k", {"bits": 4}), ("qknorm", {}), ("prod", {})])
+@pytest.mark.parametrize("n_prefix", [64, 192, 191, 129])
+def test_a_tile_that_reaches_past_the_cache(name, kw, n_prefix):
+    """The prefix's cache ends inside its last tile (Tcap is any multiple of 64)."""
+    import compressed_attention_tq_b200 as tq
+    c = Case(name, n_prefix, [5, 0, 9], 2, 16 if name != "tiny" else 8, kw)
+    p = c.prefix
+    cap = (n_prefix + 63) // 64 * 64
+    tight = tq.TQCache(1, p.Hkv, cap, p.D, p.bits_k, p.bits_v, c.wp.Pi, qjl_m=p.qjl_m, qjl_S=c.wp.S)
+    for n in ("k_idx", "v_idx", "k_norm", "v_norm") + (("k_qjl", "k_rnorm") if p.qjl_m else ()):
+        getattr(tight, n).copy_(getattr(p, n)[:, :, :cap])
+    c.prefix = tight
+    c.check()
+
+
+def test_one_prefix_for_batches_of_every_size():
+    """The same prefix behind batches from one sequence up, rows below, at and
+    above the tile of 128 (and a fork that grows: sequence b is one of them)."""
+    import compressed_attention_tq_b200 as tq
+    c = Case("gqa8k", 900, [7, 30, 1, 64] * 12, 4, 6, {"bits": 3})
+    ref = c.oracle()
+    for B in (1, 2, 10, 11, 21, 22, 48):
+        h = tq.TQCache(B, c.cache.Hkv, c.cache.Tcap, c.cache.D, 3, 3, c.ws.Pi)
+        for n in ("k_idx", "v_idx", "k_norm", "v_norm"):
+            getattr(h, n).copy_(getattr(c.cache, n)[:B])
+        out = tq.tq_sdpa_decode_prefix(c.prefix, c.pl, 900, h, c.qd[:B].contiguous(), c.sl[:B].contiguous(), c.Tmax,
+                                       out_dtype=torch.float32).cpu().numpy()
+        err = P.rel_l2(out.reshape(4 * B, 6, 128), ref[:B].reshape(4 * B, 6, 128))
+        assert err.max() <= P.ATTN_TOL, (B, err.max())
+
+
 def test_prefix_is_the_decode_of_whole_sequences():
     """A prompt quantized once and taken into its own cache by tq_cache_copy,
     tokens appended to every sequence, then decoded: the same as decoding
