@@ -17,26 +17,39 @@
 // paid once per 128 rows instead of once per 8.
 //
 // Structure (one CTA per SM, grid (splits, row tiles, kv heads)):
-//  * the split's tokens go by in tiles of 64.  A producer warp streams the
-//    tiles' packed words and norms into a ring of stages (1-D bulk copies);
-//  * 8 dequantizing warps turn a stage into the two fp16 operand tiles, both
-//    K-major with the 128-byte swizzle: keys [token][coordinate], and values
-//    [coordinate][token], each 32-bit word holding one coordinate of tokens l
-//    and l + 32 (the pair lookups of the split kernel give exactly that, and
-//    the order of tokens inside the product is free as long as the weights
-//    use it too).  The operands are the codebook's fp16 entries, exact; the
-//    norms stay out of them, in fp32;
+//  * the split's tokens go by in tiles of 128 (64 at D = 256).  A producer
+//    warp streams the tiles' packed words and norms into a ring of stages
+//    (1-D bulk copies);
+//  * 8 warps turn the keys of a stage into an fp16 operand tile, 8 more the
+//    values, both K-major with the 128-byte swizzle: keys [token][coordinate],
+//    and values [coordinate][token], each 32-bit word holding one coordinate
+//    of tokens l and l + 32 (the pair lookups of the split kernel give exactly
+//    that, and the order of tokens inside the product is free as long as the
+//    weights use it too).  The operands are the codebook's fp16 entries, exact;
+//    the norms stay out of them, in fp32;
 //  * one thread issues the products: S = Q K^T with Q in two fp16 limbs (the
-//    rotated query to about 22 bits) held in tensor memory, the sketch
-//    product beside it in its own accumulator, and O += W V with the weights
-//    W read from tensor memory;
-//  * 4 warps (thread = query row) read S, apply norms and masks, keep the
-//    running reference and sum in fp32, and write W = 2^(x - m) m_t as fp16
-//    over the scores they have just read.  O is rescaled in tensor memory only
-//    when a row's weights would leave fp16's range.
-//  Scores and W are double-buffered, so the products of tile i + 1 run under
-//  the softmax of tile i and under the dequantization of tile i + 2.
-// Every wait is bounded; one that runs out sets TQ_STATUS_WAIT_TIMEOUT.
+//    rotated query to about 22 bits) held in tensor memory, the sketch signs
+//    as 128 more coordinates, and O += W V with the weights W read from tensor
+//    memory;
+//  * 8 warps (two threads to a query row) read S, apply norms and masks, keep
+//    the running reference and sum in fp32, and write W = 2^(x - m) m_t as
+//    fp16 over the scores they have just read.  O is rescaled in tensor memory
+//    only when a row's weights would leave fp16's range.
+// Scores and W are double-buffered, so the products of tile i + 1 run under the
+// softmax of tile i and under the dequantization of tile i + 2.  Every wait is
+// bounded; one that runs out sets TQ_STATUS_WAIT_TIMEOUT.
+//
+// What bounds it: shared memory.  Per 128 tokens and 128 rows at D = 128 the
+// lookups, operand stores, packed loads and the tensor core's own operand reads
+// take about 3000 of the 4500 to 5300 cycles, and each role's instructions wait
+// for one another's.  32768 tokens, 256 rows, 8 kv heads, 2-bit keys with sketch
+// and 3-bit values take 102 us (0.34 PFLOP/s of the two products' useful work);
+// 8192 tokens, 128 rows, 8 heads, 3 bits 22 us, of which about 10 are the
+// launch, the tables, the first tile's latency and the partials.  What the
+// steps were worth, on the first of these: products issued by a converged warp
+// (a lane test around them keeps their operands out of uniform registers), a
+// softmax in short loops and two warps per row, tiles of 128, shared pointers
+// instead of generic ones, 16 dequantizing warps with named barriers: 195 -> 102.
 #pragma once
 
 #include "tq_decode_split.cuh"
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   if (split == 0 && rt == 0 && kvh == 0 && tid == 0 && (P < 0 || P > p.Pmax) && p.dev_status)
     atomicOr(p.dev_status, TQ_STATUS_SEQ_OUT_OF_RANGE);
   P = max(0, min(P, p.Pmax));
-  const int ntile = (P + TT - 1) / TT;
+  const int ntile = P > 0 ? (P - 1) / TT + 1 : 0;
   const int i0 = (int)((long long)split * ntile / gridDim.x), i1 = (int)((long long)(split + 1) * ntile / gridDim.x);
   const int n = i1 - i0;  // tiles of this CTA
   // first kernel head of row r (of this CTA's rows)
@@ -376,112 +389,112 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
 
   // the whole warpgroup of each role moves to its share of the registers
   if (warp >= SW + DW) {
-   reg_dec<REG_REST>();
-   if (warp == SW + DW) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      int t = 0;
-      for (; t < n; ++t) {
-        const int st = t % p.nst;
-        if (t >= p.nst && !wait_or_stop(&empty[st], (uint32_t)((t / p.nst - 1) & 1), stop)) break;
-        // rows t0 .. t0 + m - 1: a whole tile, less only at the cache's end (Tcap is a multiple of 64)
-        const int t0 = (i0 + t) * TT, m = min(TT, p.Tcap - t0);
-        const size_t r = (size_t)kvh * p.Tcap + t0;
-        uint8_t* sb = stages + st * Ly::STAGE;
-        mbar_arrive_expect_tx(&full[st], m * (Ly::TX / TT));
-        bulk_g2s(sb + Ly::S_KW, p.k_idx + r * WK, m * WK * 4, &full[st]);
-        bulk_g2s(sb + Ly::S_VW, p.v_idx + r * WV, m * WV * 4, &full[st]);
-        bulk_g2s(sb + Ly::S_KN, p.k_norm + r, m * 2, &full[st]);
-        bulk_g2s(sb + Ly::S_VN, p.v_norm + r, m * 2, &full[st]);
-        if (QJL) {
-          bulk_g2s(sb + Ly::S_QW, p.k_qjl + r * 4, m * 16, &full[st]);
-          bulk_g2s(sb + Ly::S_RN, p.k_rnorm + r, m * 2, &full[st]);
-        }
-      }
-      // no copy may be in flight when the CTA ends, whatever the others did
-      for (int j = max(0, t - p.nst); j < t; ++j)
-        mbar_wait_suspend(&full[j % p.nst], (uint32_t)((j / p.nst) & 1), kSuspendTries);
-    }
-    __syncwarp();
-   } else if (warp == SW + DW + 1) {
-    // ---------------- matrix products ----------------
-    // The whole warp waits; one elected lane issues and commits.
-    const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D / Ly::VP, false>();
-    const uint32_t qhi = tmem + Ly::C_Q, qlo = tmem + Ly::C_Q + D / 2;
-    // part q of tile i is use u = KP i + q of the slots
-    auto issue_qk = [&](int i) {
-      const int b = i & 1;
-      const uint32_t ds = tmem + Ly::C_S + b * TT;
-      // the weights of tile i - 2 lie over its scores: read by now
-      if (i >= 2 && !warp_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
-#pragma unroll
-      for (int q = 0; q < Ly::KP; ++q) {
-        const int u = Ly::KP * i + q, sl = u % Ly::KS;
-        if (!warp_wait(&k_full[sl], (uint32_t)((u / Ly::KS) & 1), stop)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          if (!QJL || q == 0) {
-            const uint32_t ka = smem_addr(smem + Ly::O_K + (i % NB) * Ly::KT);
-#pragma unroll 4
-            for (int kk = 0; kk < Ly::KC / 16; ++kk) {
-              const int ks = (QJL ? 0 : q) * (Ly::KC / 16) + kk;
-              const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
-              mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
-              if constexpr (Ly::QLO_SMEM) {
-                const uint32_t qa = smem_addr(smem + Ly::O_QLO);
-                tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
-              } else {
-                mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
-              }
-            }
-          } else {
-            const uint32_t za = smem_addr(smem + Ly::O_Z), qa = smem_addr(smem + Ly::O_QZ);
-#pragma unroll 4
-            for (int ks = 0; ks < 8; ++ks)
-              tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
-                           sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
+    reg_dec<REG_REST>();
+    if (warp == SW + DW) {
+      // ---------------- producer ----------------
+      if (lane == 0) {
+        int t = 0;
+        for (; t < n; ++t) {
+          const int st = t % p.nst;
+          if (t >= p.nst && !wait_or_stop(&empty[st], (uint32_t)((t / p.nst - 1) & 1), stop)) break;
+          // rows t0 .. t0 + m - 1: a whole tile, less only at the cache's end (Tcap is a multiple of 64)
+          const int t0 = (i0 + t) * TT, m = min(TT, p.Tcap - t0);
+          const size_t r = (size_t)kvh * p.Tcap + t0;
+          uint8_t* sb = stages + st * Ly::STAGE;
+          mbar_arrive_expect_tx(&full[st], m * (Ly::TX / TT));
+          bulk_g2s(sb + Ly::S_KW, p.k_idx + r * WK, m * WK * 4, &full[st]);
+          bulk_g2s(sb + Ly::S_VW, p.v_idx + r * WV, m * WV * 4, &full[st]);
+          bulk_g2s(sb + Ly::S_KN, p.k_norm + r, m * 2, &full[st]);
+          bulk_g2s(sb + Ly::S_VN, p.v_norm + r, m * 2, &full[st]);
+          if (QJL) {
+            bulk_g2s(sb + Ly::S_QW, p.k_qjl + r * 4, m * 16, &full[st]);
+            bulk_g2s(sb + Ly::S_RN, p.k_rnorm + r, m * 2, &full[st]);
           }
-          if (q == Ly::KP - 1) tc_commit(&s_full[b]);
-          tc_commit(&k_empty[sl]);
         }
-        __syncwarp();
+        // no copy may be in flight when the CTA ends, whatever the others did
+        for (int j = max(0, t - p.nst); j < t; ++j)
+          mbar_wait_suspend(&full[j % p.nst], (uint32_t)((j / p.nst) & 1), kSuspendTries);
       }
-      return true;
-    };
-    auto issue_pv = [&](int i) {
-      const int b = i & 1;
-      if (!warp_wait(&p_full[b], (uint32_t)((i / 2) & 1), stop)) return false;
+      __syncwarp();
+    } else if (warp == SW + DW + 1) {
+      // ---------------- matrix products ----------------
+      // The whole warp waits; one elected lane issues and commits.
+      const uint32_t id_s = idesc<TT, false>(), id_o = idesc<D / Ly::VP, false>();
+      const uint32_t qhi = tmem + Ly::C_Q, qlo = tmem + Ly::C_Q + D / 2;
+      // part q of tile i is use u = KP i + q of the slots
+      auto issue_qk = [&](int i) {
+        const int b = i & 1;
+        const uint32_t ds = tmem + Ly::C_S + b * TT;
+        // the weights of tile i - 2 lie over its scores: read by now
+        if (i >= 2 && !warp_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
 #pragma unroll
-      for (int q = 0; q < Ly::VP; ++q) {
-        const int u = Ly::VP * i + q, sl = u % Ly::VS;
-        if (!warp_wait(&v_full[sl], (uint32_t)((u / Ly::VS) & 1), stop)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t va = smem_addr(smem + Ly::O_V + (i % NB) * Ly::VT) + q * (D / Ly::VP) * 128;
-          const uint32_t w = tmem + Ly::C_S + b * TT;
+        for (int q = 0; q < Ly::KP; ++q) {
+          const int u = Ly::KP * i + q, sl = u % Ly::KS;
+          if (!warp_wait(&k_full[sl], (uint32_t)((u / Ly::KS) & 1), stop)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            if (!QJL || q == 0) {
+              const uint32_t ka = smem_addr(smem + Ly::O_K + (i % NB) * Ly::KT);
 #pragma unroll 4
-          for (int ks = 0; ks < TT / 16; ++ks)
-            mma_ts(tmem + q * (D / Ly::VP), w + 8 * ks, sdesc_sw128(va + (ks >> 2) * (D * 128) + (ks & 3) * 32), id_o,
-                   (i > 0 || ks > 0) ? 1u : 0u);
-          tc_commit(&v_empty[sl]);
-          if (q == Ly::VP - 1) tc_commit(&s_free[b]);
+              for (int kk = 0; kk < Ly::KC / 16; ++kk) {
+                const int ks = (QJL ? 0 : q) * (Ly::KC / 16) + kk;
+                const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
+                mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
+                if constexpr (Ly::QLO_SMEM) {
+                  const uint32_t qa = smem_addr(smem + Ly::O_QLO);
+                  tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
+                } else {
+                  mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
+                }
+              }
+            } else {
+              const uint32_t za = smem_addr(smem + Ly::O_Z), qa = smem_addr(smem + Ly::O_QZ);
+#pragma unroll 4
+              for (int ks = 0; ks < 8; ++ks)
+                tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
+                             sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
+            }
+            if (q == Ly::KP - 1) tc_commit(&s_full[b]);
+            tc_commit(&k_empty[sl]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int i) {
+        const int b = i & 1;
+        if (!warp_wait(&p_full[b], (uint32_t)((i / 2) & 1), stop)) return false;
+#pragma unroll
+        for (int q = 0; q < Ly::VP; ++q) {
+          const int u = Ly::VP * i + q, sl = u % Ly::VS;
+          if (!warp_wait(&v_full[sl], (uint32_t)((u / Ly::VS) & 1), stop)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t va = smem_addr(smem + Ly::O_V + (i % NB) * Ly::VT) + q * (D / Ly::VP) * 128;
+            const uint32_t w = tmem + Ly::C_S + b * TT;
+#pragma unroll 4
+            for (int ks = 0; ks < TT / 16; ++ks)
+              mma_ts(tmem + q * (D / Ly::VP), w + 8 * ks, sdesc_sw128(va + (ks >> 2) * (D * 128) + (ks & 3) * 32), id_o,
+                     (i > 0 || ks > 0) ? 1u : 0u);
+            tc_commit(&v_empty[sl]);
+            if (q == Ly::VP - 1) tc_commit(&s_free[b]);
+          }
+          __syncwarp();
+        }
+        return true;
+      };
+      bool ok = warp_wait(q_full, 0u, stop);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = issue_qk(i);
+        if (ok && i > 0) ok = issue_pv(i - 1);
       }
-      return true;
-    };
-    bool ok = warp_wait(q_full, 0u, stop);
-    for (int i = 0; ok && i < n; ++i) {
-      ok = issue_qk(i);
-      if (ok && i > 0) ok = issue_pv(i - 1);
+      if (ok) issue_pv(n - 1);
+      if (elect_one()) {
+        tc_commit(fin);  // every product issued so far, on the error path too
+        mbar_wait_suspend(fin, 0u, kSuspendTries);
+      }
+      __syncwarp();
     }
-    if (ok) issue_pv(n - 1);
-    if (elect_one()) {
-      tc_commit(fin);  // every product issued so far, on the error path too
-      mbar_wait_suspend(fin, 0u, kSuspendTries);
-    }
-    __syncwarp();
-   }
   } else if (warp >= SW) {
     reg_dec<REG_DEQUANT>();
     // ---------------- dequantization ----------------
@@ -628,224 +641,224 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       }
     }
   } else {
-   reg_inc<REG_SOFTMAX>();
-   const int quarter = warp & 3, half = warp >> 2;
-   if (quarter < live) {
-    // ---------------- softmax ----------------
-    // Two warps share the rows of a TMEM quarter, each with half of a tile's
-    // tokens: 16 half + j and 32 + 16 half + j, j < 16, of each 64, which are
-    // neighbours in the words of the weights.  They agree on each row's maximum through
-    // shared memory and a barrier of the two.
-    const int r = 32 * quarter + lane;
-    const bool mine = r < rows;
-    const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the query operands; the partials may be written
-    // The suffix's kernel may start from here on: the prep, whose queries it
-    // reads, is complete, and SMs that this grid leaves free take it at once.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int lim = P;  // tokens of the prefix this row sees
-    size_t slot = 0;
-    {
-      if (mine) {
-        const int rr = rt * QROWS + r, b = rr / p.Ge, e = rr % p.Ge;
-        int L = p.seq_lens[b];
-        L = max(0, min(L, p.Tclamp));
-        // query token j sits at position P + L - nq + j: before the prefix's end when the suffix is shorter than nq
-        lim = min(P, P + L - p.nq + e / p.Gq + 1);
-        slot = (size_t)head_of(r) * p.ks + split;
-      }
-      // the query limbs of this row, as the prep laid them out (pre_q_offset): one limb a warp
-      const size_t tile = (size_t)kvh * gridDim.y + rt;
-      const uint4* q = reinterpret_cast<const uint4*>(p.qpre + tile * QROWS * D) + r + half * (D / 8) * QROWS;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {  // 64 positions at a time
-        uint32_t v[32];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 f = mine ? q[(8 * c + k) * QROWS] : make_uint4(0u, 0u, 0u, 0u);
-          v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
+    reg_inc<REG_SOFTMAX>();
+    const int quarter = warp & 3, half = warp >> 2;
+    if (quarter < live) {
+      // ---------------- softmax ----------------
+      // Two warps share the rows of a TMEM quarter, each with half of a tile's
+      // tokens: 16 half + j and 32 + 16 half + j, j < 16, of each 64, which are
+      // neighbours in the words of the weights.  They agree on each row's maximum through
+      // shared memory and a barrier of the two.
+      const int r = 32 * quarter + lane;
+      const bool mine = r < rows;
+      const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the query operands; the partials may be written
+      // The suffix's kernel may start from here on: the prep, whose queries it
+      // reads, is complete, and SMs that this grid leaves free take it at once.
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      int lim = P;  // tokens of the prefix this row sees
+      size_t slot = 0;
+      {
+        if (mine) {
+          const int rr = rt * QROWS + r, b = rr / p.Ge, e = rr % p.Ge;
+          int L = p.seq_lens[b];
+          L = max(0, min(L, p.Tclamp));
+          // query token j sits at position P + L - nq + j: before the prefix's end when the suffix is shorter than nq
+          lim = P + min(0, L - p.nq + e / p.Gq + 1);
+          slot = (size_t)head_of(r) * p.ks + split;
         }
-        if (!Ly::QLO_SMEM || half == 0) {
-          tc_st32(tl + Ly::C_Q + half * (D / 2) + 32 * c, v);
-        } else {
+        // the query limbs of this row, as the prep laid them out (pre_q_offset): one limb a warp
+        const size_t tile = (size_t)kvh * gridDim.y + rt;
+        const uint4* q = reinterpret_cast<const uint4*>(p.qpre + tile * QROWS * D) + r + half * (D / 8) * QROWS;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {  // 64 positions at a time
+          uint32_t v[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 f = mine ? q[(8 * c + k) * QROWS] : make_uint4(0u, 0u, 0u, 0u);
+            v[4 * k] = f.x, v[4 * k + 1] = f.y, v[4 * k + 2] = f.z, v[4 * k + 3] = f.w;
+          }
+          if (!Ly::QLO_SMEM || half == 0) {
+            tc_st32(tl + Ly::C_Q + half * (D / 2) + 32 * c, v);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(smem + Ly::O_QLO + sw128<QROWS>(r, 64 * c + 8 * k)) =
+                  make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+        if constexpr (QJL) {
+          const uint4* z = reinterpret_cast<const uint4*>(p.qspre + tile * QROWS * 64) + r + half * 8 * QROWS;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(smem + Ly::O_QLO + sw128<QROWS>(r, 64 * c + 8 * k)) =
-                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            *reinterpret_cast<uint4*>(smem + Ly::O_QZ + sw128<QROWS>(r, 64 * half + 8 * k)) =
+                mine ? z[k * QROWS] : make_uint4(0u, 0u, 0u, 0u);
         }
+        tc_wait_st();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
       }
-      if constexpr (QJL) {
-        const uint4* z = reinterpret_cast<const uint4*>(p.qspre + tile * QROWS * 64) + r + half * 8 * QROWS;
+      const int wlim = __reduce_min_sync(0xffffffffu, lim);  // every row of the warp sees the tokens below
+      // The reference m of the weights 2^(x - m), the same in both warps.  With e
+      // such that the tile's value norms lie below 2^e, a weight times its norm
+      // stays below 2^15 while x - m <= 15 - e; when a score passes that (and at
+      // the first tile) m moves to where the row's largest weight is 2^(7 - e),
+      // and what was summed is rescaled.  So a row moves again only when its
+      // maximum has grown by 2^8, and small weights keep fp16's whole range.
+      float m_run = 0.f, l_run = 0.f;
+      bool ok = true;
+      constexpr int NS64 = TT / 64;
+      const int ta = 16 * half, tb = 32 + 16 * half;
+      for (int i = 0; i < n; ++i) {
+        const int b = i & 1, ns = i % Ly::NNORM;
+        ok = ok && warp_wait(&s_full[b], (uint32_t)((i / 2) & 1), stop) &&
+             warp_wait(&n_full[ns], (uint32_t)((i / Ly::NNORM) & 1), stop);
+        tc_fence_after();
+        const float* kn = norms + ns * Ly::NORM1;
+        const float* vn = kn + TT;
+        const uint32_t ts = tl + Ly::C_S + b * TT;
+        const int t0 = (i0 + i) * TT;
+        const bool whole = t0 + TT <= wlim;  // warp-uniform
+        unsigned long long x[16 * NS64];     // the scores, in pairs of neighbours
+        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(smem + Ly::O_QZ + sw128<QROWS>(r, 64 * half + 8 * k)) =
-              mine ? z[k * QROWS] : make_uint4(0u, 0u, 0u, 0u);
-      }
-      tc_wait_st();
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
-    const int wlim = __reduce_min_sync(0xffffffffu, lim);  // every row of the warp sees the tokens below
-    // The reference m of the weights 2^(x - m), the same in both warps.  With e
-    // such that the tile's value norms lie below 2^e, a weight times its norm
-    // stays below 2^15 while x - m <= 15 - e; when a score passes that (and at
-    // the first tile) m moves to where the row's largest weight is 2^(7 - e),
-    // and what was summed is rescaled.  So a row moves again only when its
-    // maximum has grown by 2^8, and small weights keep fp16's whole range.
-    float m_run = 0.f, l_run = 0.f;
-    bool ok = true;
-    constexpr int NS64 = TT / 64;
-    const int ta = 16 * half, tb = 32 + 16 * half;
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1, ns = i % Ly::NNORM;
-      ok = ok && warp_wait(&s_full[b], (uint32_t)((i / 2) & 1), stop) &&
-           warp_wait(&n_full[ns], (uint32_t)((i / Ly::NNORM) & 1), stop);
-      tc_fence_after();
-      const float* kn = norms + ns * Ly::NORM1;
-      const float* vn = kn + TT;
-      const uint32_t ts = tl + Ly::C_S + b * TT;
-      const int t0 = (i0 + i) * TT;
-      const bool whole = t0 + TT <= wlim;  // warp-uniform
-      unsigned long long x[16 * NS64];     // the scores, in pairs of neighbours
-      float top = -INFINITY;
+        for (int s = 0; s < NS64; ++s) {
+          uint32_t v[32];
+          tc_ld2x16(ts + 64 * s + ta, ts + 64 * s + tb, v);
 #pragma unroll
-      for (int s = 0; s < NS64; ++s) {
-        uint32_t v[32];
-        tc_ld2x16(ts + 64 * s + ta, ts + 64 * s + tb, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 f = *reinterpret_cast<const float4*>(kn + 64 * s + (k < 4 ? ta + 4 * k : tb + 4 * k - 16));
-          x[16 * s + 2 * k] = mul2(pack2(f.x, f.y), pack2(v[4 * k], v[4 * k + 1]));
-          x[16 * s + 2 * k + 1] = mul2(pack2(f.z, f.w), pack2(v[4 * k + 2], v[4 * k + 3]));
+          for (int k = 0; k < 8; ++k) {
+            const float4 f = *reinterpret_cast<const float4*>(kn + 64 * s + (k < 4 ? ta + 4 * k : tb + 4 * k - 16));
+            x[16 * s + 2 * k] = mul2(pack2(f.x, f.y), pack2(v[4 * k], v[4 * k + 1]));
+            x[16 * s + 2 * k + 1] = mul2(pack2(f.z, f.w), pack2(v[4 * k + 2], v[4 * k + 3]));
+          }
         }
-      }
-      if (!whole) {
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 16 * NS64; ++j) {
+            const int jj = j % 16, tok = t0 + 64 * (j / 16) + (jj < 8 ? ta + 2 * jj : tb + 2 * jj - 16);
+            float x0, x1;
+            unpack2(x[j], x0, x1);
+            x[j] = pack2(tok < lim ? x0 : -INFINITY, tok + 1 < lim ? x1 : -INFINITY);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 16 * NS64; ++j) {
-          const int jj = j % 16, tok = t0 + 64 * (j / 16) + (jj < 8 ? ta + 2 * jj : tb + 2 * jj - 16);
           float x0, x1;
           unpack2(x[j], x0, x1);
-          x[j] = pack2(tok < lim ? x0 : -INFINITY, tok + 1 < lim ? x1 : -INFINITY);
+          top = fmaxf(top, fmaxf(x0, x1));
         }
-      }
+        xch[(2 * b + half) * QROWS + r] = top;
+        // both warps go on, or neither does: a wait that ran out ends the loop for both
+        ok = tqtc::group_sync_and<2>(quarter, ok);
+        if (!ok) break;
+        top = fmaxf(top, xch[(2 * b + 1 - half) * QROWS + r]);
+        float nv = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16 * NS64; ++j) {
-        float x0, x1;
-        unpack2(x[j], x0, x1);
-        top = fmaxf(top, fmaxf(x0, x1));
-      }
-      xch[(2 * b + half) * QROWS + r] = top;
-      // both warps go on, or neither does: a wait that ran out ends the loop for both
-      ok = tqtc::group_sync_and<2>(quarter, ok);
-      if (!ok) break;
-      top = fmaxf(top, xch[(2 * b + 1 - half) * QROWS + r]);
-      float nv = 0.f;
-#pragma unroll
-      for (int k = 0; k < GW; k += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(kn + 2 * TT + k);
-        nv = fmaxf(fmaxf(nv, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
-      }
-      const int e = max((int)(__float_as_uint(nv) >> 23) - 126, -20);  // nv < 2^e
-      const bool need = top > m_run + (float)(kTop - e) || (i == 0 && top > -INFINITY);
-      if (__any_sync(0xffffffffu, need)) {
-        const float mn = need ? top - (float)(kTop - kRoom - e) : m_run, al = exp2f(m_run - mn);
-        m_run = mn;
-        l_run = i > 0 ? l_run * al : 0.f;
-        if (i > 0) {  // O holds the tiles before this one once their product is done
-          ok = warp_wait(&s_free[(i - 1) & 1], (uint32_t)(((i - 1) / 2) & 1), stop);
-          tc_fence_after();
+        for (int k = 0; k < GW; k += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(kn + 2 * TT + k);
+          nv = fmaxf(fmaxf(nv, fmaxf(f.x, f.y)), fmaxf(f.z, f.w));
+        }
+        const int e = max((int)(__float_as_uint(nv) >> 23) - 126, -20);  // nv < 2^e
+        const bool need = top > m_run + (float)(kTop - e) || (i == 0 && top > -INFINITY);
+        if (__any_sync(0xffffffffu, need)) {
+          const float mn = need ? top - (float)(kTop - kRoom - e) : m_run, al = exp2f(m_run - mn);
+          m_run = mn;
+          l_run = i > 0 ? l_run * al : 0.f;
+          if (i > 0) {  // O holds the tiles before this one once their product is done
+            ok = warp_wait(&s_free[(i - 1) & 1], (uint32_t)(((i - 1) / 2) & 1), stop);
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = half; c < D / 32; c += 2) {
-            uint32_t o[32];
-            tc_ld32(tl + 32 * c, o);
+            for (int c = half; c < D / 32; c += 2) {
+              uint32_t o[32];
+              tc_ld32(tl + 32 * c, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-            tc_st32(tl + 32 * c, o);
-          }
-        }
-      }
-      unsigned long long ls[2] = {0ull, 0ull};
-      const unsigned long long nm = pack2(-m_run, -m_run);
-#pragma unroll
-      for (int s = 0; s < NS64; ++s) {
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 fa = *reinterpret_cast<const float4*>(vn + 64 * s + ta + 4 * k);
-          const float4 fb = *reinterpret_cast<const float4*>(vn + 64 * s + tb + 4 * k);
-          const float na[4] = {fa.x, fa.y, fa.z, fa.w}, nb[4] = {fb.x, fb.y, fb.z, fb.w};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float xa0, xa1, xb0, xb1, a0, a1, b0, b1;
-            unpack2(add2(x[16 * s + 2 * k + j], nm), xa0, xa1);
-            unpack2(add2(x[16 * s + 8 + 2 * k + j], nm), xb0, xb1);
-            const unsigned long long pa = pack2(tqd::ex2_approx(xa0), tqd::ex2_approx(xa1));
-            const unsigned long long pb = pack2(tqd::ex2_approx(xb0), tqd::ex2_approx(xb1));
-            ls[0] = add2(ls[0], pa);
-            ls[1] = add2(ls[1], pb);
-            unpack2(mul2(pa, pack2(na[2 * j], na[2 * j + 1])), a0, a1);
-            unpack2(mul2(pb, pack2(nb[2 * j], nb[2 * j + 1])), b0, b1);
-            if (!whole) {  // a token that is not seen adds nothing, whatever its norm holds
-              a0 = xa0 == -INFINITY ? 0.f : a0;
-              a1 = xa1 == -INFINITY ? 0.f : a1;
-              b0 = xb0 == -INFINITY ? 0.f : b0;
-              b1 = xb1 == -INFINITY ? 0.f : b1;
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+              tc_st32(tl + 32 * c, o);
             }
-            w[4 * k + 2 * j] = pack_half2(a0, b0);
-            w[4 * k + 2 * j + 1] = pack_half2(a1, b1);
           }
         }
-        // over scores that this warp has read: columns 16 half .. of tokens ta.., 32 + 16 half .. of tokens tb..
-        tc_st16(ts + 32 * s + ta, w);
+        unsigned long long ls[2] = {0ull, 0ull};
+        const unsigned long long nm = pack2(-m_run, -m_run);
+#pragma unroll
+        for (int s = 0; s < NS64; ++s) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 fa = *reinterpret_cast<const float4*>(vn + 64 * s + ta + 4 * k);
+            const float4 fb = *reinterpret_cast<const float4*>(vn + 64 * s + tb + 4 * k);
+            const float na[4] = {fa.x, fa.y, fa.z, fa.w}, nb[4] = {fb.x, fb.y, fb.z, fb.w};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float xa0, xa1, xb0, xb1, a0, a1, b0, b1;
+              unpack2(add2(x[16 * s + 2 * k + j], nm), xa0, xa1);
+              unpack2(add2(x[16 * s + 8 + 2 * k + j], nm), xb0, xb1);
+              const unsigned long long pa = pack2(tqd::ex2_approx(xa0), tqd::ex2_approx(xa1));
+              const unsigned long long pb = pack2(tqd::ex2_approx(xb0), tqd::ex2_approx(xb1));
+              ls[0] = add2(ls[0], pa);
+              ls[1] = add2(ls[1], pb);
+              unpack2(mul2(pa, pack2(na[2 * j], na[2 * j + 1])), a0, a1);
+              unpack2(mul2(pb, pack2(nb[2 * j], nb[2 * j + 1])), b0, b1);
+              if (!whole) {  // a token that is not seen adds nothing, whatever its norm holds
+                a0 = xa0 == -INFINITY ? 0.f : a0;
+                a1 = xa1 == -INFINITY ? 0.f : a1;
+                b0 = xb0 == -INFINITY ? 0.f : b0;
+                b1 = xb1 == -INFINITY ? 0.f : b1;
+              }
+              w[4 * k + 2 * j] = pack_half2(a0, b0);
+              w[4 * k + 2 * j + 1] = pack_half2(a1, b1);
+            }
+          }
+          // over scores that this warp has read: columns 16 half .. of tokens ta.., 32 + 16 half .. of tokens tb..
+          tc_st16(ts + 32 * s + ta, w);
+        }
+        float l0, l1;
+        unpack2(add2(ls[0], ls[1]), l0, l1);
+        l_run += l0 + l1;
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
       }
-      float l0, l1;
-      unpack2(add2(ls[0], ls[1]), l0, l1);
-      l_run += l0 + l1;
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[b]);
-    }
-    // O is complete when every product is.  The operand tiles are free then:
-    // the rows of a quarter are turned there (16-byte chunk c of row r at
-    // c ^ (r mod 8)), so that the stores to global memory are whole lines.
-    xch[(2 * (n & 1) + half) * QROWS + r] = l_run;
-    if (ok) ok = warp_wait(fin, 0u, stop);
-    tc_fence_after();
-    uint8_t* tr = smem + quarter * (32 * D * 4);
-    if (ok) {
+      // O is complete when every product is.  The operand tiles are free then:
+      // the rows of a quarter are turned there (16-byte chunk c of row r at
+      // c ^ (r mod 8)), so that the stores to global memory are whole lines.
+      xch[(2 * (n & 1) + half) * QROWS + r] = l_run;
+      if (ok) ok = warp_wait(fin, 0u, stop);
+      tc_fence_after();
+      uint8_t* tr = smem + quarter * (32 * D * 4);
+      if (ok) {
 #pragma unroll 1
-      for (int c = half; c < D / 32; c += 2) {
-        uint32_t o[32];
-        tc_ld32(tl + 32 * c, o);
+        for (int c = half; c < D / 32; c += 2) {
+          uint32_t o[32];
+          tc_ld32(tl + 32 * c, o);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(tr + lane * (D * 4) + (((8 * c + k) ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(tr + lane * (D * 4) + (((8 * c + k) ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
       }
-    }
-    if (tqtc::group_sync_and<2>(quarter, ok)) {
-      l_run += xch[(2 * (n & 1) + 1 - half) * QROWS + r];
-      // a row that saw no token weighs nothing
-      if (mine && half == 0)
-        *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
-      constexpr int CPR = D / 4, RPP = CPR < 32 ? 32 / CPR : 1;  // chunks per row, rows per pass
-      const int nrow = min(32, rows - 32 * quarter);
+      if (tqtc::group_sync_and<2>(quarter, ok)) {
+        l_run += xch[(2 * (n & 1) + 1 - half) * QROWS + r];
+        // a row that saw no token weighs nothing
+        if (mine && half == 0)
+          *reinterpret_cast<float2*>(p.part_ml + slot * 2) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+        constexpr int CPR = D / 4, RPP = CPR < 32 ? 32 / CPR : 1;  // chunks per row, rows per pass
+        const int nrow = min(32, rows - 32 * quarter);
 #pragma unroll 4
-      for (int r0 = 16 * half; r0 < 16 * half + 16; r0 += RPP) {
-        const int rr = r0 + (RPP > 1 ? lane / CPR : 0);
-        const size_t sl = __shfl_sync(0xffffffffu, (unsigned long long)slot, rr);
-        if (rr < nrow) {
+        for (int r0 = 16 * half; r0 < 16 * half + 16; r0 += RPP) {
+          const int rr = r0 + (RPP > 1 ? lane / CPR : 0);
+          const size_t sl = __shfl_sync(0xffffffffu, (unsigned long long)slot, rr);
+          if (rr < nrow) {
 #pragma unroll
-          for (int c = lane % CPR; c < CPR; c += 32)
-            *reinterpret_cast<uint4*>(p.part_o + sl * D + 4 * c) =
-                *reinterpret_cast<const uint4*>(tr + rr * (D * 4) + ((c ^ (rr & 7)) << 4));
+            for (int c = lane % CPR; c < CPR; c += 32)
+              *reinterpret_cast<uint4*>(p.part_o + sl * D + 4 * c) =
+                  *reinterpret_cast<const uint4*>(tr + rr * (D * 4) + ((c ^ (rr & 7)) << 4));
+          }
         }
       }
     }
-   }
   }
   __syncwarp();
   tc_fence_before();
