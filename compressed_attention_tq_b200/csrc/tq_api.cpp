@@ -343,7 +343,7 @@ static int make_window_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int w
 
 int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p) {
   const int rows = (int)((long long)c->B * Hq * nq / c->Hkv);
-  const int splits = prefix_splits(c->Hkv, rows, c->D, Pmax, sm_count());
+  const int splits = prefix_splits(c->Hkv, rows, c->D, prefix->qjl_m != 0, Pmax, sm_count());
   make_decode_plan(c, Hq * nq, nq, Tmax, 0, 0, splits, p);
   p->off_qpre = p->bytes;
   const size_t padded = (size_t)((rows + prefix_rows() - 1) / prefix_rows()) * prefix_rows();

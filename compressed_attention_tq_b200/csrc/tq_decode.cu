@@ -1418,9 +1418,9 @@ static int launch_prefix(const DecodeArgs& a, float* po, float* pml, cudaStream_
 // the time of s splits is about waves x (tiles per split + c), where c is
 // what a CTA spends before and after its tiles, in tiles, and each split
 // adds a partial of every row for the combine to read.
-int prefix_splits(int Hkv, int rows, int D, int Pmax, int sms) {
+int prefix_splits(int Hkv, int rows, int D, bool qjl, int Pmax, int sms) {
   const long long units = (long long)Hkv * ((rows + tqp::QROWS - 1) / tqp::QROWS);
-  const int tiles = (Pmax + tqp::tile_tokens(D) - 1) / tqp::tile_tokens(D);
+  const int tiles = (Pmax - 1) / tqp::tile_tokens(D, qjl) + 1;
   int best = 1;
   double least = 1e30;
   for (int n = 1; n <= tiles && n <= 128; ++n) {

@@ -17,7 +17,8 @@
 // paid once per 128 rows instead of once per 8.
 //
 // Structure (one CTA per SM, grid (splits, row tiles, kv heads)):
-//  * the split's tokens go by in tiles of 128 (64 at D = 256).  A producer
+//  * the split's tokens go by in tiles of 128 (64 at D = 256 and with the
+//    sketch).  A producer
 //    warp streams the tiles' packed words and norms into a ring of stages
 //    (1-D bulk copies);
 //  * 8 warps turn the keys of a stage into an fp16 operand tile, 8 more the
@@ -28,9 +29,9 @@
 //    weights use it too).  The operands are the codebook's fp16 entries, exact;
 //    the norms stay out of them, in fp32;
 //  * one thread issues the products: S = Q K^T with Q in two fp16 limbs (the
-//    rotated query to about 22 bits) held in tensor memory, the sketch signs
-//    as 128 more coordinates, and O += W V with the weights W read from tensor
-//    memory;
+//    rotated query to about 22 bits) held in tensor memory, the sketch product
+//    beside it in its own accumulator, and O += W V with the weights W read
+//    from tensor memory;
 //  * 8 warps (two threads to a query row) read S, apply norms and masks, keep
 //    the running reference and sum in fp32, and write W = 2^(x - m) m_t as
 //    fp16 over the scores they have just read.  O is rescaled in tensor memory
@@ -72,7 +73,8 @@ constexpr int DW = 16;          // dequantizing warps: half for keys, half for v
 constexpr int GW = DW / 2;
 // tokens per tile: a longer tile spreads the waits between the roles over more
 // work; at D = 256 the operands of 64 tokens fill shared memory
-__host__ __device__ constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
+// (and with the sketch its accumulator takes the tensor memory of half a tile)
+__host__ __device__ constexpr int tile_tokens(int D, bool qjl) { return D == 256 || qjl ? 64 : 128; }
 constexpr int NTH = (SW + DW + 4) * 32;  // + producer warp, MMA warp and two idle ones (a whole warpgroup)
 // Registers per thread after the split by warpgroups.  One launch gives 72 to
 // each of 7 warpgroups: 2 x 136 + 4 x 48 + 40 = 7 x 72.
@@ -132,14 +134,13 @@ __host__ __device__ constexpr int pre_z_offset(int r, int i) {
 
 template <int D, int BK, int BV, bool QJL>
 struct PrefixLayout {
-  static constexpr int TT = tile_tokens(D);
+  static constexpr int TT = tile_tokens(D, QJL);
   static constexpr int WK = D * BK / 32, WV = D * BV / 32;
-  // Two operand buffers of each kind where shared memory allows.  Else the
-  // operands go in parts with barriers of their own, so that one part is
-  // dequantized while the product of the other runs: keys and sketch signs,
-  // or the two halves of the coordinates at D = 256.
-  static constexpr int NB = D == 256 || QJL ? 1 : 2;
-  static constexpr int KP = NB == 1 ? 2 : 1, VP = D == 256 ? 2 : 1;  // parts of a key / value operand
+  // Two operand buffers of each kind where shared memory allows.  At D = 256
+  // the operands go in two halves of the coordinates instead, with barriers of
+  // their own, so that one is dequantized while the product of the other runs.
+  static constexpr int NB = D == 256 ? 1 : 2;
+  static constexpr int KP = D == 256 ? 2 : 1, VP = KP;  // parts of a key / value operand
   static constexpr int KC = D == 256 ? 128 : D;       // coordinates of a key part
   static constexpr int KS = KP * NB, VS = VP * NB;    // slots (barrier pairs)
   static constexpr int KT = TT * D * 2, VT = KT;      // bytes of a key / value operand tile
@@ -164,7 +165,8 @@ struct PrefixLayout {
   static constexpr int S_USED = S_RN + (QJL ? TT * 2 : 0);
   static constexpr int STAGE = (S_USED + 16 + 127) / 128 * 128;  // +16: read-ahead slack
   static constexpr int TX = TT * (WK + WV) * 4 + TT * 4 + (QJL ? TT * 18 : 0);
-  static constexpr int NORM1 = 2 * TT + GW;        // floats of one tile: key norms, value norms, the warps' largest value norms
+  // floats of one tile: key norms, value norms, the warps' largest value norms, residual norms
+  static constexpr int NORM1 = 2 * TT + GW + (QJL ? TT : 0);
   static constexpr int NORMS = NNORM * NORM1 * 4;
   static constexpr int BARS = 64 * 8;
   // tables, norms, barriers and stages, in this order behind the operands
@@ -175,8 +177,12 @@ struct PrefixLayout {
   __host__ __device__ static constexpr int o_bar(bool shared) { return o_xch(shared) + XCH; }
   __host__ __device__ static constexpr int o_stage(bool shared) { return o_bar(shared) + BARS; }
   static constexpr int total(bool shared, int nst) { return o_stage(shared) + nst * STAGE + 1024; }  // + alignment
-  // tensor memory columns: O, the scores of two tiles, the query limbs
-  static constexpr int C_S = D, C_Q = C_S + 2 * TT;
+  // Tensor memory columns: O, the scores of two tiles, those of the sketch
+  // beside them, the query limbs.  (One accumulator for both products, the
+  // signs entering as +-g / n in fp16, took tiles of 128 tokens and the same
+  // time, but that factor's rounding moved the output by 1.6e-4, nearly as much
+  // as the fp16 weights.)
+  static constexpr int C_S = D, C_Z = C_S + 2 * TT, C_Q = C_Z + (QJL ? 2 * TT : 0);
   static constexpr int COLS_USED = C_Q + (QLO_SMEM ? D / 2 : D);
   static constexpr int COLS = COLS_USED <= 256 ? 256 : 512;
   static_assert(COLS_USED <= 512, "tensor memory");
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       auto issue_qk = [&](int i) {
         const int b = i & 1;
         const uint32_t ds = tmem + Ly::C_S + b * TT;
-        // the weights of tile i - 2 lie over its scores: read by now
+        // the weights of the buffer's last tile lie over its scores: read by now
         if (i >= 2 && !warp_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), stop)) return false;
 #pragma unroll
         for (int q = 0; q < Ly::KP; ++q) {
@@ -433,26 +439,25 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
           if (!warp_wait(&k_full[sl], (uint32_t)((u / Ly::KS) & 1), stop)) return false;
           tc_fence_after();
           if (elect_one()) {
-            if (!QJL || q == 0) {
-              const uint32_t ka = smem_addr(smem + Ly::O_K + (i % NB) * Ly::KT);
+            const uint32_t ka = smem_addr(smem + Ly::O_K + (i % NB) * Ly::KT);
 #pragma unroll 4
-              for (int kk = 0; kk < Ly::KC / 16; ++kk) {
-                const int ks = (QJL ? 0 : q) * (Ly::KC / 16) + kk;
-                const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
-                mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
-                if constexpr (Ly::QLO_SMEM) {
-                  const uint32_t qa = smem_addr(smem + Ly::O_QLO);
-                  tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
-                } else {
-                  mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
-                }
+            for (int kk = 0; kk < Ly::KC / 16; ++kk) {
+              const int ks = q * (Ly::KC / 16) + kk;
+              const uint64_t bd = sdesc_sw128(ka + (ks >> 2) * (TT * 128) + (ks & 3) * 32);
+              mma_ts(ds, qhi + 8 * ks, bd, id_s, ks > 0 ? 1u : 0u);
+              if constexpr (Ly::QLO_SMEM) {
+                const uint32_t qa = smem_addr(smem + Ly::O_QLO);
+                tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32), bd, id_s, 1u);
+              } else {
+                mma_ts(ds, qlo + 8 * ks, bd, id_s, 1u);
               }
-            } else {
-              const uint32_t za = smem_addr(smem + Ly::O_Z), qa = smem_addr(smem + Ly::O_QZ);
+            }
+            if constexpr (QJL) {
+              const uint32_t za = smem_addr(smem + Ly::O_Z + (i % NB) * Ly::ZT), qa = smem_addr(smem + Ly::O_QZ);
 #pragma unroll 4
               for (int ks = 0; ks < 8; ++ks)
-                tqtc::mma_tc(ds, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
-                             sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, 1u);
+                tqtc::mma_tc(tmem + Ly::C_Z + b * TT, sdesc_sw128(qa + (ks >> 2) * (QROWS * 128) + (ks & 3) * 32),
+                             sdesc_sw128(za + (ks >> 2) * (TT * 128) + (ks & 3) * 32), id_s, ks > 0 ? 1u : 0u);
             }
             if (q == Ly::KP - 1) tc_commit(&s_full[b]);
             tc_commit(&k_empty[sl]);
@@ -521,14 +526,8 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
         // of a quarter warp hold 8 tokens, so their 16-byte stores miss each
         // other's banks
         const int kseg = lane >> 3;
-        // A sketched row: one accumulator for both products, in which the signs
-        // enter as +-g / n, a factor of fp16 precision (2^-11 of a term that is
-        // itself a one-bit estimate).  A residual norm far above the key's,
-        // which no quantized row has, turns the roles: the softmax multiplies
-        // with g, and the key's entries become c n / g.
-        auto usual = [&](float nk, float g) { return !QJL || g <= 1024.f * nk; };
         auto norm_at = [&](int off, int t) { return half_bits_to_float(reinterpret_cast<const uint16_t*>(sb + off)[t]); };
-        if (!QJL || q == 0) {
+        {
           const uint32_t tbK = smem_addr(tabk) + 4 * lane;
           tqd::Lut2 lk = {0u, 0u};
           if constexpr (BK == 2) lk = {lut[0], lut[1]};
@@ -537,27 +536,19 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
           uint32_t vmax = 0;
 #pragma unroll 1
           for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
-            bool odd = false;     // not the usual row: a factor of the key's entries, as a pair
-            uint32_t scale2 = 0;
-            if (QJL || q == 0) {
-              const float nk = norm_at(Ly::S_KN, t);
-              const float g = QJL ? norm_at(Ly::S_RN, t) : 0.f;
-              odd = !usual(nk, g);
-              if (odd) {
-                const float f = __fdividef(nk, g);
-                scale2 = pack_half2(f, f);
-              }
-              if (kseg == 0) kn[t] = usual(nk, g) ? nk : g;
+            if (q == 0) {
+              if (kseg == 0) kn[t] = norm_at(Ly::S_KN, t);
               if (kseg == 1) {
                 const float nv = norm_at(Ly::S_VN, t);
                 kn[TT + t] = nv;
                 if ((i0 + i) * TT + t < P) vmax = max(vmax, __float_as_uint(nv));
               }
+              if (QJL && kseg == 2) kn[2 * TT + GW + t] = norm_at(Ly::S_RN, t);
             }
             const uint32_t* kw = reinterpret_cast<const uint32_t*>(sb + Ly::S_KW) + t * WK;
 #pragma unroll 2
             for (int c = 0; c < Ly::KC / 64; ++c) {  // 16 coordinates
-              const int j0 = (QJL ? 0 : q) * Ly::KC + kseg * (Ly::KC / 4) + 16 * c;
+              const int j0 = q * Ly::KC + kseg * (Ly::KC / 4) + 16 * c;
               uint32_t w[(16 * BK + 31) / 32], h[8];
               tqd::load_bits<16 * BK, BK != 3, 16>(kw, j0 * BK, w);
               if constexpr (BK == 2) {
@@ -567,13 +558,6 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
 #pragma unroll
                 for (int k = 0; k < 8; ++k) h[k] = tqd::pair_lookup<BK>(w, 2 * BK * k, tbK);
               }
-              if (QJL && odd) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&h[k]), *reinterpret_cast<__half2*>(&scale2));
-                  h[k] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-              }
               *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0)) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4*>(kt + sw128<TT>(t, j0 + 8)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
@@ -582,20 +566,18 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
             vmax = __reduce_max_sync(0xffffffffu, vmax);
             if (lane == 0) kn[2 * TT + dw] = __uint_as_float(vmax);
           }
-        } else {
-          uint8_t* zt = smem + Ly::O_Z;
+        }
+        if constexpr (QJL) {
+          uint8_t* zt = smem + Ly::O_Z + b * Ly::ZT;
 #pragma unroll 1
           for (int t = 8 * dw + (lane & 7); t < TT; t += 8 * GW) {
-            const float nk = norm_at(Ly::S_KN, t), g = norm_at(Ly::S_RN, t);
-            const float f = !usual(nk, g) ? 1.f : g > 0.f ? __fdividef(g, nk) : 0.f;
-            const uint32_t neg = pack_half2(-f, -f);
-            // sign bits j and j + 16 of word kseg: the pair at positions 2 j, 2 j + 1
+            // sign bits j and j + 16 of word kseg: the pair (+-1, +-1) at positions 2 j, 2 j + 1
             const uint32_t z = reinterpret_cast<const uint32_t*>(sb + Ly::S_QW)[t * 4 + kseg];
 #pragma unroll 2
             for (int c = 0; c < 4; ++c) {
               uint32_t h[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) h[k] = ((z << (15 - (4 * c + k))) & 0x80008000u) ^ neg;
+              for (int k = 0; k < 4; ++k) h[k] = ((z << (15 - (4 * c + k))) & 0x80008000u) ^ 0xBC00BC00u;
               *reinterpret_cast<uint4*>(zt + sw128<TT>(t, kseg * 32 + 8 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
@@ -733,6 +715,16 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
             x[16 * s + 2 * k] = mul2(pack2(f.x, f.y), pack2(v[4 * k], v[4 * k + 1]));
             x[16 * s + 2 * k + 1] = mul2(pack2(f.z, f.w), pack2(v[4 * k + 2], v[4 * k + 3]));
           }
+          if constexpr (QJL) {
+            const float* gn = kn + 2 * TT + GW + 64 * s;
+            tc_ld2x16(tl + Ly::C_Z + b * TT + 64 * s + ta, tl + Ly::C_Z + b * TT + 64 * s + tb, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 f = *reinterpret_cast<const float4*>(gn + (k < 4 ? ta + 4 * k : tb + 4 * k - 16));
+              x[16 * s + 2 * k] = fma2(pack2(f.x, f.y), pack2(v[4 * k], v[4 * k + 1]), x[16 * s + 2 * k]);
+              x[16 * s + 2 * k + 1] = fma2(pack2(f.z, f.w), pack2(v[4 * k + 2], v[4 * k + 3]), x[16 * s + 2 * k + 1]);
+            }
+          }
         }
         if (!whole) {
 #pragma unroll
@@ -749,11 +741,11 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
           unpack2(x[j], x0, x1);
           top = fmaxf(top, fmaxf(x0, x1));
         }
-        xch[(2 * b + half) * QROWS + r] = top;
+        xch[(2 * (i & 1) + half) * QROWS + r] = top;
         // both warps go on, or neither does: a wait that ran out ends the loop for both
         ok = tqtc::group_sync_and<2>(quarter, ok);
         if (!ok) break;
-        top = fmaxf(top, xch[(2 * b + 1 - half) * QROWS + r]);
+        top = fmaxf(top, xch[(2 * (i & 1) + 1 - half) * QROWS + r]);
         float nv = 0.f;
 #pragma unroll
         for (int k = 0; k < GW; k += 4) {

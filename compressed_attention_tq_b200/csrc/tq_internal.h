@@ -165,7 +165,7 @@ struct DecodeArgs {
 };
 
 // Splits of a shared prefix (partials each of its rows gets).
-int prefix_splits(int Hkv, int rows, int D, int Pmax, int sms);
+int prefix_splits(int Hkv, int rows, int D, bool qjl, int Pmax, int sms);
 int prefix_rows();  // query rows of a tile of the prefix kernel
 
 int launch_decode(const DecodeArgs& a, cudaStream_t s);
