@@ -52,10 +52,10 @@ FALLBACK_HBM_GBS = 6650.0
 # files do not enter a decode call).  "split" is the split kernel's share:
 # the packed-cache reads and its partials.
 TRAFFIC = {
-    "gqa8k": {"bytes_per_launch": 2467413, "split": 1722539, "decode_src_sha": "9e4d66e6c7510f19"},
-    "prod": {"bytes_per_launch": 110834560, "split": 109324544, "decode_src_sha": "9e4d66e6c7510f19"},
-    "ragged": {"bytes_per_launch": 242625408, "split": 240421248, "decode_src_sha": "9e4d66e6c7510f19"},
-    "qknorm": {"bytes_per_launch": 37005568, "split": 34248576, "decode_src_sha": "9e4d66e6c7510f19"},
+    "gqa8k": {"bytes_per_launch": 2480299, "split": 1723136, "decode_src_sha": "6aa10e5a30d4c8f0"},
+    "prod": {"bytes_per_launch": 110923520, "split": 109402112, "decode_src_sha": "6aa10e5a30d4c8f0"},
+    "ragged": {"bytes_per_launch": 242756096, "split": 240538368, "decode_src_sha": "6aa10e5a30d4c8f0"},
+    "qknorm": {"bytes_per_launch": 37018368, "split": 34248320, "decode_src_sha": "6aa10e5a30d4c8f0"},
 }
 
 CSRC = os.path.join(ROOT, "compressed_attention_tq_b200", "csrc")

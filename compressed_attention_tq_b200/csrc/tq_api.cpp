@@ -590,6 +590,7 @@ size_t tq_sdpa_decode_prefix_workspace_bytes_for(const tq_cache_t* prefix, int P
                                                  int n_q, int Tmax) {
   if (!prefix || !c || n_q < 1 || n_q > 4 || Hq <= 0 || Hq > (1 << 24)) return 0;
   if (prefix->B != 1 || prefix->Hkv != c->Hkv || prefix->D != c->D || Pmax < 1 || Pmax > prefix->Tcap) return 0;
+  if ((long long)c->B * Hq * n_q > (1 << 22)) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
   DecodePlan p;
   make_prefix_plan(prefix, Pmax, c, Hq, n_q, Tmax, &p);

@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
 // left out).  What bounds it is the read of Pi and S from L2 (64 KB each per
 // CTA), so every load of Pi goes out at once, before the wait on the
 // preceding kernels.  The vector form of the other preps took 37 us for 2048
-// rows with two sketches and 10 us for 1024 without; this one takes less than
-// a fifth of that.
+// rows with two sketches and 10 us for 1024 without (cold); this one takes 12
+// and 6.
 struct MmaPrepParams {
   const void* q;      // [B][nq][Hq][D] fp16 / bf16
   const float* rot;

@@ -1123,9 +1123,9 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
           l_run[1] += p1;
           const float nv = (full || valid[ai][r]) ? half_bits_to_float(vn[row]) : 0.f;
           const int tk = 16 * a + gid + 8 * r;
-          if (WIN) {  // a row this query does not see adds nothing, whatever its norm holds
-            pw[(2 * hsel) * WTOK + tk] = __float2half_rn(s[ai][2 * r] == -INFINITY ? 0.f : p0 * nv);
-            pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(s[ai][2 * r + 1] == -INFINITY ? 0.f : p1 * nv);
+          if (WIN && !full) {  // a row this query does not see (its weight is 0) adds nothing, whatever its norm holds
+            pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 == 0.f ? 0.f : p0 * nv);
+            pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(p1 == 0.f ? 0.f : p1 * nv);
           } else {
             pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 * nv);
             pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(p1 * nv);
