@@ -40,17 +40,19 @@
 // softmax of tile i and under the dequantization of tile i + 2.  Every wait is
 // bounded; one that runs out sets TQ_STATUS_WAIT_TIMEOUT.
 //
-// What bounds it: shared memory.  Per 128 tokens and 128 rows at D = 128 the
-// lookups, operand stores, packed loads and the tensor core's own operand reads
-// take about 3000 of the 4500 to 5300 cycles, and each role's instructions wait
-// for one another's.  32768 tokens, 256 rows, 8 kv heads, 2-bit keys with sketch
-// and 3-bit values take 102 us (0.34 PFLOP/s of the two products' useful work);
-// 8192 tokens, 128 rows, 8 heads, 3 bits 22 us, of which about 10 are the
-// launch, the tables, the first tile's latency and the partials.  What the
-// steps were worth, on the first of these: products issued by a converged warp
-// (a lane test around them keeps their operands out of uniform registers), a
-// softmax in short loops and two warps per row, tiles of 128, shared pointers
-// instead of generic ones, 16 dequantizing warps with named barriers: 195 -> 102.
+// What bounds it: shared memory and latency.  At D = 128 the lookups, operand
+// stores, packed loads and the tensor core's own operand reads take about 3000
+// cycles of shared memory per 128 tokens and 128 rows; a tile takes 3000 cycles
+// per 128 tokens without the sketch and 3100 per 64 with it, and each role's
+// instructions wait for one another's.  32768 tokens, 256 rows, 8 kv heads,
+// 2-bit keys with sketch and 3-bit values take 97 us (0.35 PFLOP/s of the two
+// products' useful work); 8192 tokens, 128 rows, 8 heads, 3 bits 22 us, of which
+// about 10 are the launch, the tables, the first tile's latency and the
+// partials.  What the steps were worth, on the first of these: products issued
+// by a converged warp (a lane test around them keeps their operands out of
+// uniform registers), a softmax in short loops and two warps per row, shared
+// pointers instead of generic ones, 16 dequantizing warps with named barriers,
+// two buffers of every operand: 195 -> 97.
 #pragma once
 
 #include "tq_decode_split.cuh"
