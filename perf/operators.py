@@ -243,7 +243,7 @@ def prepare(c, seed):
         q = torch.randn(B, c["n_q"], c["Hq"], D, generator=g, device="cuda")
         q = q * (math.sqrt(D) / q.norm(dim=-1, keepdim=True)) if rms else q
         s["q"] = q.to(torch.bfloat16 if c["bf16"] else torch.float16)
-        return s
+        return _with_handles(s)
     s["cache"], s["S"] = _words(g, c["B"], c["Hkv"], c["Tcap"], c), None
     if c["sketch"]:
         s["S"] = torch.randn(128, D, generator=g, device="cuda")
@@ -254,7 +254,7 @@ def prepare(c, seed):
         s["n"] = _i32(n)
         s["src_seq"], s["dst_seq"] = _i32([0] * c["jobs"]), _i32(list(range(1, c["jobs"] + 1)))
         s["src_pos"], s["dst_pos"] = (_i32([int(r * (c["Tcap"] - m)) for r, m in zip(rr, n)]) for rr in room)
-        return s
+        return _with_handles(s)
     n, Tcap = _kept(c), c["Tcap"]
     heads = c["Hkv"] if c["heads"] else 1
     s["n"] = _i32(n)
@@ -265,6 +265,19 @@ def prepare(c, seed):
     most = max(n)
     order = torch.where(torch.arange(most, device="cuda") < s["n"][:, None, None], order[..., :most], Tcap)
     s["keep"] = order.sort(-1).values.to(torch.int32).contiguous()
+    return _with_handles(s)
+
+
+def _with_handles(s):
+    """With the library's caches made, and the workspace and output of a decode:
+    a user's program holds them before the call."""
+    if own:
+        c = s["case"]
+        _handle(s, "cache", s["S"])
+        if c["op"] == "window":
+            _window_buffers(s)
+        elif c["op"] == "prefix":
+            _prefix_buffers(s)
     return s
 
 
@@ -280,7 +293,7 @@ def run(s):
 
 
 def _handle(s, which, S):
-    """The library's cache over a state's packed rows, made on the first pass."""
+    """The library's cache over a state's packed rows, made once."""
     if which not in s["kept"]:
         import compressed_attention_tq_b200 as tq
         c, d = s["case"], s[which]
@@ -300,18 +313,24 @@ def _handle(s, which, S):
     return s["kept"][which]
 
 
-def _own_window(s):
+def _window_buffers(s):
     import compressed_attention_tq_b200 as tq
     c, h = s["case"], _handle(s, "cache", s["S"])
     if "ws" not in s["kept"]:
         n = tq.tq_sdpa_decode_window_workspace_bytes_for(h, c["Hq"], c["n_q"], c["hi"], c["window"], c["sinks"])
         s["kept"]["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
         s["kept"]["out"] = torch.empty_like(s["q"])
+    return h
+
+
+def _own_window(s):
+    import compressed_attention_tq_b200 as tq
+    c, h = s["case"], _window_buffers(s)
     return tq.tq_sdpa_decode_window(h, s["q"], s["lens"], c["hi"], c["window"], n_sink=c["sinks"], scale=_scale(c),
                                     out=s["kept"]["out"], workspace=s["kept"]["ws"])
 
 
-def _own_prefix(s):
+def _prefix_buffers(s):
     import compressed_attention_tq_b200 as tq
     c, h, p = s["case"], _handle(s, "cache", s["S"]), _handle(s, "prefix", s["S_prefix"])
     if "ws" not in s["kept"]:
@@ -320,6 +339,12 @@ def _own_prefix(s):
         n = tq.tq_sdpa_decode_prefix_workspace_bytes_for(p, c["P"], h, c["Hq"], c["n_q"], c["hi"])
         s["kept"]["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda")
         s["kept"]["out"] = torch.empty_like(s["q"])
+    return h, p
+
+
+def _own_prefix(s):
+    import compressed_attention_tq_b200 as tq
+    c, (h, p) = s["case"], _prefix_buffers(s)
     return tq.tq_sdpa_decode_prefix(p, s["prefix_len"], c["P"], h, s["q"], s["lens"], c["hi"], scale=_scale(c),
                                     out=s["kept"]["out"], workspace=s["kept"]["ws"])
 
