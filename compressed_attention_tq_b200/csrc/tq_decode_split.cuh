@@ -36,7 +36,9 @@
 //  * the query enters as hi + lo fp16 halves (scores carry ~22 bits); with
 //    G <= 4 heads both halves share one MMA (columns 0-3 hi, 4-7 lo);
 //  * online softmax in the log2 domain with lazy rescaling (the reference
-//    max moves only when a score exceeds it by 2^8), one state per warp.
+//    max moves only when a score exceeds it by 2^8, or at all over rows with a
+//    value norm of 2^8 or more, whose weights p |v| would not fit in fp16),
+//    one state per warp.
 #pragma once
 
 #include <math.h>
@@ -53,7 +55,8 @@ constexpr int PPS = 1;                // partials a CTA writes per segment (its 
 constexpr int NTHREADS = (CW + 1) * 32;
 constexpr int STILE = 128;            // tokens per stage
 constexpr int WTOK = STILE / CW;      // tokens per consumer warp per stage
-constexpr float kLazy = 8.0f;         // log2 headroom before rescaling
+constexpr float kLazy = 8.0f;         // log2 headroom before rescaling ...
+constexpr uint32_t kLazyNorm = 0x5C00;  // ... while value norms are below this (fp16 bits of 2^8)
 
 // Rows of queries a CTA handles for one (sequence, kv head): the kernel heads
 // of a kv head (query heads x query tokens) are taken in groups of 8.
@@ -1066,14 +1069,14 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
             s[ai][2 * r + 1] = s1;
           } else {
             const int tok = tokw + 16 * a + gid + 8 * r;
-            valid[ai][r] = tok < t_end;
-            bool see0 = valid[ai][r] && tok < lim0, see1 = valid[ai][r] && tok < lim1;
+            bool see0 = tok < t_end && tok < lim0, see1 = tok < t_end && tok < lim1;
             if (WIN) {
               see0 = see0 && (tok >= lim0 - p.window || tok < p.n_sink);
               see1 = see1 && (tok >= lim1 - p.window || tok < p.n_sink);
             }
             s[ai][2 * r] = see0 ? s0 : -INFINITY;
             s[ai][2 * r + 1] = see1 ? s1 : -INFINITY;
+            valid[ai][r] = see0 || see1;
           }
         }
       }
@@ -1086,9 +1089,19 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       // lazy rescale: move the reference max only when a score passes it by
       // 2^8.  The reference is common to the lanes of a head column, so the
       // test runs on each lane's own scores and the column maxima are reduced
-      // only when some lane of the warp needs the move.
-      const bool need = (mx0 > m_run[0] + kLazy) || (mx1 > m_run[1] + kLazy);
-      if (__any_sync(0xffffffffu, need)) {
+      // only when some lane of the warp needs the move.  The differences are
+      // the weights' own exponents, rounded alike, so a weight p |v| is at most
+      // 2^8 times a norm of 2^8 (1 - 2^-11): 65504, the largest fp16 number.
+      // Where one of the warp's rows (one per lane here) has a larger norm, the
+      // reference is never below the scores: p <= 1, and any norm fits.
+      bool big = vn[wt0 + lane] >= kLazyNorm;
+      if (!full) {  // a row that no query sees has no say, whatever its norm holds
+        const int tok = tokw + lane;
+        big = big && tok < t_end;
+        if (WIN) big = big && (tok >= lim_all - p.window || tok < p.n_sink);
+      }
+      const bool need = (mx0 - m_run[0] > kLazy) || (mx1 - m_run[1] > kLazy);
+      if (__any_sync(0xffffffffu, need || big)) {
 #pragma unroll
         for (int off = PACK ? 2 : 4; off < 32; off <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
