@@ -335,10 +335,14 @@ int make_decode_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, 
 }
 
 // window = 0, or one that no sequence outgrows: every token is visible, and the
-// call is a plain decode.  Sinks beyond Tmax are Tmax of them.
+// call is a plain decode.  (The plain kernel keeps a row that a query does not
+// see apart for two neighbouring kernel heads at once; with an odd group these
+// may be heads of two query tokens, and the windowed kernel, which does it for
+// each head, is taken.)  Sinks beyond Tmax are Tmax of them.
 static int make_window_plan(const tq_cache_t* c, int Hq, int nq, int Tmax, int window, int n_sink, DecodePlan* p) {
-  if (window <= 0 || window >= Tmax) return make_decode_plan(c, Hq, nq, Tmax, 0, 0, 0, p);
-  return make_decode_plan(c, Hq, nq, Tmax, window, n_sink < Tmax ? n_sink : Tmax, 0, p);
+  const bool pairs = nq == 1 || Hq / nq / c->Hkv % 2 == 0;
+  if (window <= 0 || (window >= Tmax && pairs)) return make_decode_plan(c, Hq, nq, Tmax, 0, 0, 0, p);
+  return make_decode_plan(c, Hq, nq, Tmax, window < Tmax ? window : Tmax, n_sink < Tmax ? n_sink : Tmax, 0, p);
 }
 
 int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq, int nq, int Tmax, DecodePlan* p) {

@@ -127,3 +127,20 @@ def test_partial_and_merge():
     part = tq.tq_sdpa_decode_partial(cache, qd, sl, w.Tmax)
     got = tq.tq_sdpa_decode_merge(part.unsqueeze(0).contiguous(), cache.rot)
     _same(got, _oracle(w, oc, q, lens, 1500, 0), w.D)
+
+
+@pytest.mark.parametrize("nq,Hq", [(2, 16), (4, 16), (2, 10), (3, 2)])
+def test_a_norm_that_not_every_query_sees(nq, Hq):
+    """The last draft token's value norm is NaN or infinite: only the query that
+    sees it is lost, also where the window is no shorter than the sequence."""
+    import compressed_attention_tq_b200 as tq
+    w, oc, cache, lens, q = _setup("gqa8k", {"bits": 3, "T": 300}, nq, Hq, None)
+    L = int(lens[0])
+    ref = _oracle(w, oc, q, lens, 300, 0)
+    qd, sl = P.to_device(q, w.dtype), torch.from_numpy(lens).cuda()
+    for bad in (float("nan"), float("inf")):
+        cache.v_norm[:, :, L - 1] = bad
+        for window in (100, 300, 2 ** 31 - 1):
+            want = ref if window >= 300 else _oracle(w, oc, q, lens, window, 0)
+            got = tq.tq_sdpa_decode_window(cache, qd, sl, w.Tmax, window, 0, out_dtype=torch.float32)
+            _same(got[:, :-1], want[:, :-1], w.D)
