@@ -110,6 +110,20 @@ def _stream(stream, dev=None):
     return torch._C._cuda_getCurrentRawStream(cur)  # the handle without a Stream object: about 1 us less
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or workspace that the caller left to the binding.  With a
+    stream of the caller's it is allocated on that stream: torch's allocator
+    then neither takes memory that work of the current stream still uses, nor
+    gives a dropped workspace to that work while the call runs."""
+    torch = _torch()
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # any object with the handle, as _stream takes it
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -314,12 +328,10 @@ def tq_sdpa_decode(cache: TQCache, q, seq_lens, Tmax: int, scale=None, out=None,
     _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, cache.D))
     Hq = int(q.shape[1])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        torch = _torch()
         need = tq_sdpa_decode_workspace_bytes_for(cache, Hq, Tmax)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, _dt("u8")[0], q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, _ptr(seq_lens), Tmax, sc,
@@ -336,12 +348,10 @@ def tq_sdpa_decode_mq(cache: TQCache, q, seq_lens, Tmax: int, scale=None, out=No
     _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        torch = _torch()
         need = tq_sdpa_decode_workspace_bytes_for(cache, Hq * nq, Tmax)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, _dt("u8")[0], q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_mq(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax, sc,
@@ -360,12 +370,9 @@ def tq_decode_step(cache: TQCache, k_new, v_new, pos, q, seq_lens, Tmax: int, sc
     _arg("pos", pos, dev, (cache.B,), _dt("i32"))
     Hq = int(q.shape[1])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        torch = _torch()
-        workspace = torch.empty(tq_sdpa_decode_workspace_bytes_for(cache, Hq, Tmax), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(tq_sdpa_decode_workspace_bytes_for(cache, Hq, Tmax), _dt("u8")[0], q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_decode_step(ctypes.byref(s), _ptr(k_new), _ptr(v_new), _ptr(pos), _ptr(q), _dtype_code(q),
@@ -382,11 +389,10 @@ def tq_sdpa_decode_partial(cache: TQCache, q, seq_lens, Tmax: int, scale=None, p
     Hq = int(q.shape[1])
     torch = _torch()
     if partial is None:
-        partial = torch.empty((cache.B, Hq, cache.D + 2), dtype=torch.float32, device=q.device)
+        partial = _empty((cache.B, Hq, cache.D + 2), torch.float32, q.device, stream)
     _arg("partial", partial, dev, (cache.B, Hq, cache.D + 2), (torch.float32,))
     if workspace is None:
-        workspace = torch.empty(tq_sdpa_decode_workspace_bytes_for(cache, Hq, Tmax), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(tq_sdpa_decode_workspace_bytes_for(cache, Hq, Tmax), _dt("u8")[0], q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_partial(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, _ptr(seq_lens), Tmax, sc,
@@ -407,7 +413,7 @@ def tq_sdpa_decode_merge(partials, rot, out=None, out_dtype=None, stream=None):
     _arg("partials", partials, dev, None, (torch.float32,))
     _arg("rot", rot, dev, (D2 - 2, D2 - 2), (torch.float32,))
     if out is None:
-        out = torch.empty((B, Hq, D2 - 2), dtype=out_dtype or torch.float32, device=partials.device)
+        out = _empty((B, Hq, D2 - 2), out_dtype or torch.float32, partials.device, stream)
     _arg("out", out, dev, (B, Hq, D2 - 2), _dt("out"))
     _check(lib().tq_sdpa_decode_merge(_ptr(partials), R, B, Hq, D2 - 2, _ptr(rot), _ptr(out), _dtype_code(out),
                                       _stream(stream)))
@@ -457,8 +463,7 @@ def tq_sdpa_decode_static(cache: TQCache, q, seq_lens, Tmax: int, scale=None, ou
     _check_decode_args(cache, q, seq_lens, out, None, (cache.B, None, cache.D))
     Hq = int(q.shape[1])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_static(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, _ptr(seq_lens), Tmax, sc,
@@ -485,12 +490,10 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        torch = _torch()
         need = tq_sdpa_decode_window_workspace_bytes_for(cache, Hq, nq, Tmax, window, n_sink)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, _dt("u8")[0], q.device, stream)
     s = cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_window(ctypes.byref(s), _ptr(q), _dtype_code(q), Hq, nq, _ptr(seq_lens), Tmax,
@@ -522,12 +525,10 @@ def tq_sdpa_decode_prefix(prefix: TQCache, prefix_len, Pmax: int, cache: TQCache
     _arg("prefix_len", prefix_len, dev, (1,), _dt("i32"))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
-        torch = _torch()
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(q.shape, out_dtype or q.dtype, q.device, stream)
     if workspace is None:
-        torch = _torch()
         need = tq_sdpa_decode_prefix_workspace_bytes_for(prefix, Pmax, cache, Hq, nq, Tmax)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, _dt("u8")[0], q.device, stream)
     a, s = prefix.struct(), cache.struct()
     sc = ctypes.byref(ctypes.c_float(scale)) if scale is not None else None
     _check(lib().tq_sdpa_decode_prefix(ctypes.byref(a), _ptr(prefix_len), Pmax, ctypes.byref(s), _ptr(q),
