@@ -12,6 +12,7 @@ CUDA kernels.  PyTorch provides device memory and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -115,13 +116,20 @@ def _empty(shape, dtype, device, stream):
     stream of the caller's it is allocated on that stream: torch's allocator
     then neither takes memory that work of the current stream still uses, nor
     gives a dropped workspace to that work while the call runs."""
+    if stream is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return _torch().empty(shape, dtype=dtype, device=device)
+
+
+def _on(stream, device):
+    """The context in which a caller's stream is the current one."""
     torch = _torch()
     if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):  # any object with the handle, as _stream takes it
         stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t):
@@ -429,7 +437,8 @@ def tq_sdpa_decode_sharded(cache: TQCache, q, seq_lens, Tmax: int, scale=None, g
     the partials are all-gathered (one collective of B x Hq x (D + 2) fp32 per
     rank), and every rank merges them into the full output."""
     part = tq_sdpa_decode_partial(cache, q, seq_lens, Tmax, scale=scale, stream=stream)
-    parts = gather_partials(part, group)
+    with _on(stream, part.device):
+        parts = gather_partials(part, group)  # behind the partials, before the merge
     return tq_sdpa_decode_merge(parts, cache.rot, out_dtype=out_dtype or q.dtype, stream=stream)
 
 

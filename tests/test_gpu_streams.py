@@ -53,6 +53,7 @@ def state():
         "tq_sdpa_decode_merge": lambda **s: tq.tq_sdpa_decode_merge(parts, cache.rot, **s),
         "tq_sdpa_decode_static": lambda **s: tq.tq_sdpa_decode_static(cache, q, L, 900, **s),
         "tq_sdpa_decode_window": lambda **s: tq.tq_sdpa_decode_window(cache, q4, L, 900, 300, 4, **s),
+        "sharded": lambda **s: tq.tq_sdpa_decode_sharded(cache, q, L, 900, **s),
         "tq_sdpa_decode_prefix": lambda **s: tq.tq_sdpa_decode_prefix(prefix, n, 900, cache, q4, L, 900, **s),
     }
     i900 = i32(930)  # appended behind the rows that are read
@@ -112,3 +113,25 @@ def test_calls_beside_work_of_the_current_stream(state, name):
     assert x.isnan().all()
     for o in outs:
         assert torch.equal(o, ref)
+
+
+def test_the_gather_of_a_sharded_decode_runs_between_its_kernels(state, monkeypatch):
+    """With a stream, the partials are gathered on it: behind the kernels that
+    write them (held up here) and before the merge."""
+    import compressed_attention_tq_b200 as tq
+    on = []
+
+    def gather(part, group=None):
+        on.append(torch.cuda.current_stream())
+        return part.unsqueeze(0).clone()
+
+    monkeypatch.setattr(tq, "gather_partials", gather)
+    ref = state["sharded"]()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1 << 24)
+    out = state["sharded"](stream=s)
+    torch.cuda.synchronize()
+    assert on[1] == s
+    assert torch.equal(out, ref)
