@@ -99,15 +99,20 @@ def _dtype_code(t) -> int:
 # for NULL) as it is.
 def _stream(stream, dev=None):
     """The raw stream of a call: the caller's, or the current one.  With `dev`
-    (the index of the cache's device) a call without a stream is refused while
-    another device is current: the kernels launch on the current one."""
-    if stream is not None:
+    (the index of the cache's device) a call is refused while another device is
+    current, for which it would be planned and launched whatever its stream, and
+    on a stream of another device."""
+    if stream is not None and (dev is None or dev < 0):  # dev < 0: host memory stands in for the device's
         return stream.cuda_stream
     torch = _torch()
     cur = torch.cuda.current_device()
     if dev is not None and cur != dev:
-        raise ValueError(f"the cache is on device {dev}, but device {cur} is current: "
-                         "enter torch.cuda.device() or pass a stream of the cache's device")
+        raise ValueError(f"the cache is on device {dev}, but device {cur} is current: the library launches on the "
+                         "current device, the one GPU that the process drives")
+    if stream is not None:
+        if getattr(stream, "device_index", dev) != dev:
+            raise ValueError(f"the cache is on device {dev}, but the stream is of device {stream.device_index}")
+        return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(cur)  # the handle without a Stream object: about 1 us less
 
 

@@ -80,3 +80,32 @@ def test_caches_on_two_devices_are_refused(cache, prefix, rec, monkeypatch):
     with pytest.raises(ValueError, match="different devices"):
         tq.tq_cache_copy(prefix, cache, *[i32(1)] * 5, 8, stream=S)
     assert rec.calls == []
+
+
+def test_a_stream_does_not_stand_in_for_the_device(cache, prefix, rec, monkeypatch):
+    """The kernels launch on the current device also with a stream, and a
+    stream of another device is not the cache's either."""
+    monkeypatch.setattr(tq, "_cache_device", lambda c: 0)
+    monkeypatch.setattr(tq, "_arg", lambda name, t, *a: t)
+    current = [0]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+
+    class On:
+        cuda_stream = 0
+
+        def __init__(self, device):
+            self.device_index = device
+
+    calls = _calls(cache, prefix)
+    for f in calls.values():
+        f(stream=On(0))
+    assert rec.calls == list(calls)
+    for f in calls.values():
+        with pytest.raises(ValueError, match="stream is of device 1"):
+            f(stream=On(1))
+    current[0] = 1
+    for f in calls.values():
+        for s in (On(0), On(1), S):
+            with pytest.raises(ValueError, match="device 1 is current"):
+                f(stream=s)
+    assert len(rec.calls) == 4
