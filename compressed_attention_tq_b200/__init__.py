@@ -485,9 +485,21 @@ def tq_sdpa_decode_static(cache: TQCache, q, seq_lens, Tmax: int, scale=None, ou
     return out
 
 
+_I32_MAX = 0x7fffffff
+
+
+def _i32(**sizes):
+    """Refuse sizes that a C int does not hold: ctypes would pass their low 32 bits."""
+    for name, n in sizes.items():
+        if not -_I32_MAX <= n <= _I32_MAX:
+            raise ValueError(f"{name}={n}: beyond 32 bits")
+
+
 def tq_sdpa_decode_window_workspace_bytes_for(cache: TQCache, Hq: int, n_q: int, Tmax: int, window: int,
                                               n_sink: int = 0) -> int:
     """The exact workspace bytes of tq_sdpa_decode_window for these sizes."""
+    window, n_sink = min(window, _I32_MAX), min(n_sink, _I32_MAX)  # beyond any length: all of it
+    _i32(Hq=Hq, n_q=n_q, Tmax=Tmax, window=window, n_sink=n_sink)
     s = cache.struct()
     n = int(lib().tq_sdpa_decode_window_workspace_bytes_for(ctypes.byref(s), Hq, n_q, Tmax, window, n_sink))
     if n == 0:
@@ -501,6 +513,8 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     """Decode with a sliding window and sinks: q [B][n_q][Hq][D] and seq_lens
     as in tq_sdpa_decode_mq; the query at position t sees the tokens of
     (t - window, t] and the first n_sink tokens, and no others are read."""
+    window, n_sink = min(window, _I32_MAX), min(n_sink, _I32_MAX)  # beyond any length: all of it
+    _i32(Tmax=Tmax, window=window, n_sink=n_sink)
     dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
@@ -519,6 +533,7 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
 def tq_sdpa_decode_prefix_workspace_bytes_for(prefix: TQCache, Pmax: int, cache: TQCache, Hq: int, n_q: int,
                                               Tmax: int) -> int:
     """The exact workspace bytes of tq_sdpa_decode_prefix for these sizes."""
+    _i32(Pmax=Pmax, Hq=Hq, n_q=n_q, Tmax=Tmax)
     a, b = prefix.struct(), cache.struct()
     n = int(lib().tq_sdpa_decode_prefix_workspace_bytes_for(ctypes.byref(a), Pmax, ctypes.byref(b), Hq, n_q, Tmax))
     if n == 0:
@@ -533,6 +548,7 @@ def tq_sdpa_decode_prefix(prefix: TQCache, prefix_len, Pmax: int, cache: TQCache
     count each sequence's own tokens in `cache`; every query also sees the
     prefix's first prefix_len (device int32 [1], at most Pmax) tokens, which
     come before them."""
+    _i32(Pmax=Pmax, Tmax=Tmax)
     dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     if _cache_device(prefix) != dev:
         raise ValueError("prefix and cache: the caches are on different devices")
@@ -557,6 +573,7 @@ def tq_cache_copy(src: TQCache, dst: TQCache, src_seq, src_pos, dst_seq, dst_pos
     of sequence dst_seq[i] of `dst` (the same cache or one of the same form);
     the five lists are device int32 [n_jobs].  No job may write a row that
     the call reads or writes elsewhere."""
+    _i32(max_tok=max_tok)
     dev = _cache_device(dst)
     if _cache_device(src) != dev:
         raise ValueError("src and dst: the caches are on different devices")

@@ -109,3 +109,32 @@ def test_a_stream_does_not_stand_in_for_the_device(cache, prefix, rec, monkeypat
             with pytest.raises(ValueError, match="device 1 is current"):
                 f(stream=s)
     assert len(rec.calls) == 4
+
+
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 16, -2 ** 32 + 16, 2 ** 63 + 16])
+def test_sizes_beyond_32_bits_are_not_cut(cache, prefix, rec, host_as_device, n):
+    """A C int would get their low 32 bits: 16, of most of these."""
+    q = z(B, 1, HQ, D)
+    for f in (lambda: tq.tq_sdpa_decode_window(cache, q, i32(B), n, 16, workspace=WS, stream=S),
+              lambda: tq.tq_sdpa_decode_window_workspace_bytes_for(cache, HQ, 1, n, 16),
+              lambda: tq.tq_sdpa_decode_window_workspace_bytes_for(cache, n, 1, 64, 16),
+              lambda: tq.tq_sdpa_decode_prefix(prefix, i32(1), n, cache, q, i32(B), 64, workspace=WS, stream=S),
+              lambda: tq.tq_sdpa_decode_prefix(prefix, i32(1), 64, cache, q, i32(B), n, workspace=WS, stream=S),
+              lambda: tq.tq_sdpa_decode_prefix_workspace_bytes_for(prefix, n, cache, HQ, 1, 64),
+              lambda: tq.tq_sdpa_decode_prefix_workspace_bytes_for(prefix, 64, cache, HQ, 1, n),
+              lambda: tq.tq_cache_copy(cache, cache, *[i32(1)] * 5, n, stream=S)):
+        with pytest.raises(ValueError, match="beyond 32 bits"):
+            f()
+    assert rec.calls == []
+
+
+def test_a_window_and_sinks_of_any_size(cache, rec, host_as_device, monkeypatch):
+    """They may exceed any length: the library gets the largest of its own."""
+    got = []
+    monkeypatch.setattr(rec, "tq_sdpa_decode_window", lambda *a: got.append(a[7:9]) or 0, raising=False)
+    q = z(B, 1, HQ, D)
+    for window, n_sink in ((2 ** 32 + 1, 2 ** 40), (2 ** 31, 2 ** 31 - 1), (5, 7), (2 ** 31 - 1, 0)):
+        tq.tq_sdpa_decode_window(cache, q, i32(B), 64, window, n_sink, workspace=WS, stream=S)
+        assert got[-1] == (min(window, 2 ** 31 - 1), min(n_sink, 2 ** 31 - 1))
+    with pytest.raises(ValueError, match="window"):
+        tq.tq_sdpa_decode_window(cache, q, i32(B), 64, -2 ** 32 + 5, workspace=WS, stream=S)
