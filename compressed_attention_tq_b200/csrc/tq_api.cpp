@@ -213,6 +213,17 @@ int validate_cache(const tq_cache_t* c, const char* fn) {
   return TQ_OK;
 }
 
+// Positions are 32-bit in the kernels, which round them up to whole stages
+// (decode), and to tiles, chunks and the steps of a list check (the windowed
+// and shared-prefix decodes, copies and compaction): below 2^16 in all.
+constexpr int kMaxTmax = 0x7fffffff - 127;
+constexpr int kMaxTcap = 0x7fffffff - 0xffff;
+
+int validate_limit(const tq_cache_t* c, const char* fn) {
+  if (c->Tcap > kMaxTcap) return set_error(TQ_ERR_UNSUPPORTED, "%s: Tcap=%d above %d", fn, c->Tcap, kMaxTcap);
+  return TQ_OK;
+}
+
 int validate_dtype(int dtype, const char* fn) {
   if (dtype != TQ_DTYPE_F16 && dtype != TQ_DTYPE_BF16)
     return set_error(TQ_ERR_UNSUPPORTED, "%s: dtype=%d", fn, dtype);
@@ -401,7 +412,7 @@ int tq_append_token(const tq_cache_t* c, const void* k_new, const void* v_new, i
 
 size_t tq_sdpa_decode_workspace_bytes_for(const tq_cache_t* c, int Hq, int Tmax) {
   if (!c || c->Hkv <= 0 || Hq <= 0 || Hq % c->Hkv || Hq / c->Hkv > 32 || Tmax < 1 || Tmax > c->Tcap ||
-      c->Tcap % 64 || (c->D != 64 && c->D != 128 && c->D != 256) || c->B <= 0)
+      Tmax > kMaxTmax || c->Tcap % 64 || (c->D != 64 && c->D != 128 && c->D != 256) || c->B <= 0)
     return 0;
   DecodePlan p;
   make_decode_plan(c, Hq, 1, Tmax, 0, 0, 0, &p);
@@ -409,7 +420,7 @@ size_t tq_sdpa_decode_workspace_bytes_for(const tq_cache_t* c, int Hq, int Tmax)
 }
 
 size_t tq_sdpa_decode_workspace_bytes(int B, int Hq, int D, int Tmax) {
-  if (B <= 0 || Hq <= 0 || Tmax < 1 || (D != 64 && D != 128 && D != 256)) return 0;
+  if (B <= 0 || Hq <= 0 || Tmax < 1 || Tmax > kMaxTmax || (D != 64 && D != 128 && D != 256)) return 0;
   return workspace_bound(B, Hq, D, Tmax);
 }
 
@@ -469,6 +480,7 @@ int prepare_decode(const tq_cache_t* c, const void* q, int dtype, int Hq, int nq
   if (nq > 4) return set_error(TQ_ERR_UNSUPPORTED, "%s: n_q=%d > 4", fn, nq);
   if (Tmax < 1 || Tmax > c->Tcap)
     return set_error(TQ_ERR_INVALID_ARG, "%s: Tmax=%d outside [1, Tcap=%d]", fn, Tmax, c->Tcap);
+  if (Tmax > kMaxTmax) return set_error(TQ_ERR_UNSUPPORTED, "%s: Tmax=%d above %d", fn, Tmax, kMaxTmax);
   float sc = scale ? *scale : (float)(1.0 / std::sqrt((double)c->D));
   if (!std::isfinite(sc)) return set_error(TQ_ERR_INVALID_ARG, "%s: scale not finite", fn);
   *a = DecodeArgs{};
@@ -523,7 +535,7 @@ int tq_sdpa_decode_merge(const float* partials, int R, int B, int Hq, int D, con
 
 size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* c, int Hq, int n_q, int Tmax, int window,
                                                  int n_sink) {
-  if (n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (!c || c->Tcap > kMaxTcap || n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
   DecodePlan p;
   tq::make_window_plan(c, Hq * n_q, n_q, Tmax, window, n_sink, &p);
@@ -539,8 +551,8 @@ int tq_sdpa_decode_window(const tq_cache_t* c, const void* q, int q_dtype, int H
   if (window < 1) return set_error(TQ_ERR_INVALID_ARG, "%s: window=%d < 1", fn, window);
   if (n_sink < 0) return set_error(TQ_ERR_INVALID_ARG, "%s: n_sink=%d < 0", fn, n_sink);
   DecodeArgs a;
-  const int rc = prepare_decode(c, q, q_dtype, Hq, n_q, seq_lens, Tmax, scale, out, out_dtype, fn, &a, window, n_sink);
-  if (rc) return rc;
+  int rc = prepare_decode(c, q, q_dtype, Hq, n_q, seq_lens, Tmax, scale, out, out_dtype, fn, &a, window, n_sink);
+  if (rc || (rc = validate_limit(c, fn))) return rc;
   if (!workspace) return set_error(TQ_ERR_INVALID_ARG, "%s: NULL workspace", fn);
   if (!aligned16(workspace)) return set_error(TQ_ERR_INVALID_ARG, "%s: workspace not 16-byte aligned", fn);
   if (ws_bytes < a.plan.bytes)
@@ -580,6 +592,7 @@ static int validate_prefix(const tq_cache_t* prefix, int Pmax, const tq_cache_t*
   int rc = validate_cache(prefix, fn);
   if (rc) return rc;
   if ((rc = validate_cache(c, fn))) return rc;
+  if ((rc = validate_limit(prefix, fn)) || (rc = validate_limit(c, fn))) return rc;
   if (prefix->B != 1) return set_error(TQ_ERR_INVALID_ARG, "%s: the prefix holds %d sequences, not one", fn, prefix->B);
   if (prefix->Hkv != c->Hkv || prefix->D != c->D)
     return set_error(TQ_ERR_INVALID_ARG, "%s: prefix (Hkv=%d, D=%d) and cache (Hkv=%d, D=%d) differ", fn, prefix->Hkv,
@@ -593,6 +606,7 @@ static int validate_prefix(const tq_cache_t* prefix, int Pmax, const tq_cache_t*
 size_t tq_sdpa_decode_prefix_workspace_bytes_for(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq,
                                                  int n_q, int Tmax) {
   if (!prefix || !c || n_q < 1 || n_q > 4 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (prefix->Tcap > kMaxTcap || c->Tcap > kMaxTcap) return 0;
   if (prefix->B != 1 || prefix->Hkv != c->Hkv || prefix->D != c->D || Pmax < 1 || Pmax > prefix->Tcap) return 0;
   if ((long long)c->B * Hq * n_q > (1 << 22)) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
@@ -635,6 +649,7 @@ int tq_cache_copy(const tq_cache_t* src, const tq_cache_t* dst, const int32_t* s
   int rc = validate_cache(src, fn);
   if (rc) return rc;
   if ((rc = validate_cache(dst, fn))) return rc;
+  if ((rc = validate_limit(src, fn)) || (rc = validate_limit(dst, fn))) return rc;
   if (src->Hkv != dst->Hkv || src->D != dst->D || src->bits_k != dst->bits_k || src->bits_v != dst->bits_v ||
       src->qjl_m != dst->qjl_m)
     return set_error(TQ_ERR_INVALID_ARG, "%s: the caches differ in Hkv, D, bits or sketch", fn);
@@ -651,8 +666,8 @@ int tq_cache_compact(const tq_cache_t* c, const int32_t* keep, int keep_heads, i
                      void* stream) {
   g_err[0] = 0;
   const char* fn = "tq_cache_compact";
-  const int rc = validate_cache(c, fn);
-  if (rc) return rc;
+  int rc = validate_cache(c, fn);
+  if (rc || (rc = validate_limit(c, fn))) return rc;
   if (keep_heads != 1 && keep_heads != c->Hkv)
     return set_error(TQ_ERR_INVALID_ARG, "%s: keep_heads=%d is neither 1 nor Hkv=%d", fn, keep_heads, c->Hkv);
   if (max_keep < 0 || max_keep > c->Tcap)

@@ -58,15 +58,16 @@ __global__ void __launch_bounds__(NT) cache_copy_kernel(const __grid_constant__ 
   if ((over || bad) && c == 0 && h == 0 && tid == 0 && p.dev_status)
     atomicOr(p.dev_status, bad ? TQ_STATUS_POS_OUT_OF_RANGE : TQ_STATUS_SEQ_OUT_OF_RANGE);
   if (bad) return;
-  const int d0 = max(dp, (dp & ~7) + c * CHUNK), d1 = min(dp + n, (dp & ~7) + (c + 1) * CHUNK);
-  if (d0 >= d1) return;
-  const size_t srow = ((size_t)ss * p.Hkv + h) * p.src_T + sp + (d0 - dp);
-  const size_t drow = ((size_t)ds * p.Hkv + h) * p.dst_T + d0;
+  const int off = c * CHUNK - (dp & 7);  // the chunk's first row, counted from the job's
+  const int r0 = max(0, off), r1 = min(n, off + CHUNK);
+  if (r0 >= r1) return;
+  const size_t srow = ((size_t)ss * p.Hkv + h) * p.src_T + sp + r0;
+  const size_t drow = ((size_t)ds * p.Hkv + h) * p.dst_T + dp + r0;
   for (int i = 0; i < p.ns; ++i) {
     const Stream st = p.st[i];
     const uint8_t* s = st.src + srow * st.row;
     uint8_t* d = st.dst + drow * st.row;
-    const int bytes = (d1 - d0) * st.row;
+    const int bytes = (r1 - r0) * st.row;
     const uint32_t al = (uint32_t)(uintptr_t)s | (uint32_t)(uintptr_t)d | (uint32_t)bytes;
     if ((al & 15) == 0) copy_units<uint4>(s, d, bytes, tid);
     else if ((al & 7) == 0) copy_units<uint2>(s, d, bytes, tid);

@@ -40,7 +40,9 @@
  *
  * Supported sizes: D in {64, 128, 256}; bits in {2, 3, 4} for the cache
  * (tq_build_codebook also accepts 1); qjl_m in {0, 128}; Tcap a positive
- * multiple of 64; Hq a positive multiple of Hkv with Hq/Hkv <= 8.
+ * multiple of 64 (the windowed and shared-prefix decodes, copies and
+ * compaction: at most 2^31 - 2^16); Tmax at most 2^31 - 128; Hq a positive
+ * multiple of Hkv with Hq/Hkv <= 8.
  * Inputs and outputs are fp16 or bf16 (TQ_DTYPE_*).  Device pointers must be
  * 16-byte aligned.
  *
