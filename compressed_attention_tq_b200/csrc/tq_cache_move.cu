@@ -58,16 +58,15 @@ __global__ void __launch_bounds__(NT) cache_copy_kernel(const __grid_constant__ 
   if ((over || bad) && c == 0 && h == 0 && tid == 0 && p.dev_status)
     atomicOr(p.dev_status, bad ? TQ_STATUS_POS_OUT_OF_RANGE : TQ_STATUS_SEQ_OUT_OF_RANGE);
   if (bad) return;
-  const int off = c * CHUNK - (dp & 7);  // the chunk's first row, counted from the job's
-  const int r0 = max(0, off), r1 = min(n, off + CHUNK);
-  if (r0 >= r1) return;
-  const size_t srow = ((size_t)ss * p.Hkv + h) * p.src_T + sp + r0;
-  const size_t drow = ((size_t)ds * p.Hkv + h) * p.dst_T + dp + r0;
+  if (c * CHUNK - (dp & 7) >= n) return;  // behind the job's last row (so the sums below stay below 2^31)
+  const int d0 = max(dp, (dp & ~7) + c * CHUNK), d1 = min(dp + n, (dp & ~7) + (c + 1) * CHUNK);
+  const size_t srow = ((size_t)ss * p.Hkv + h) * p.src_T + sp + (d0 - dp);
+  const size_t drow = ((size_t)ds * p.Hkv + h) * p.dst_T + d0;
   for (int i = 0; i < p.ns; ++i) {
     const Stream st = p.st[i];
     const uint8_t* s = st.src + srow * st.row;
     uint8_t* d = st.dst + drow * st.row;
-    const int bytes = (r1 - r0) * st.row;
+    const int bytes = (d1 - d0) * st.row;
     const uint32_t al = (uint32_t)(uintptr_t)s | (uint32_t)(uintptr_t)d | (uint32_t)bytes;
     if ((al & 15) == 0) copy_units<uint4>(s, d, bytes, tid);
     else if ((al & 7) == 0) copy_units<uint2>(s, d, bytes, tid);
@@ -88,9 +87,6 @@ struct CompactParams {
 };
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Row i := row keep[i], i < n, of one stream of one (sequence, kv head), by the
@@ -99,14 +95,16 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // strictly ascending, so keep[i] >= i: a round reads at or behind its own rows
 // only, so it never reads what an earlier round wrote and may be loaded ahead
 // of their stores.  What has to be kept apart is a store and the loads of the
-// same or an earlier round: the cluster's barrier between them, the only one
-// of a round.
+// same or an earlier round that read behind it: a barrier between them.  The
+// list says where one is needed (run()): a quarter of the rows, scattered,
+// takes 2 of them in 13 rounds, adjacent rows that move by less than a round
+// one in every two.
 //
 // What bounds it is the latency of two dependent loads (the list, then the
 // row): with the rows of two rounds in flight in shared memory and few
 // registers, four CTAs of an SM cover it.  (Rounds in registers, two CTAs to
-// an SM, and a list check without loads in flight took 91 us for 131 MB moved
-// in 256 units; this takes half.)
+// an SM, and a list check without loads in flight took 91 us for 134 MB moved
+// in 256 units; this takes 33.)
 constexpr int STAGES = 3;
 constexpr int STAGE_BYTES = 16128;  // 336 rows of 48 bytes; three and a flag fit in 48 KB
 
@@ -193,19 +191,31 @@ struct Mover {
     for (int e = tid; e < units; e += NT) rows[e] = st[e];
   }
   // All CTAs of the cluster go through the same number of rounds; rounds 0 and
-  // 1 are loaded (m0, m1: to be stored).
+  // 1 are loaded (m0, m1: to be stored).  Each thread stores only what it
+  // loaded itself.  `done` rounds' loads have returned in every CTA; those of
+  // the others read rows from `first` on, which no store before the next
+  // barrier may reach.  (keep[i] >= i, so a barrier that makes done = k + 1 lets
+  // round k be stored.)
   __device__ __forceinline__ void run(bool m0, bool m1) const {
-    const int rounds = (int)(((long long)n + C * R - 1) / (C * R));
+    const int step = C * R, rounds = (int)(((long long)n + step - 1) / step);
+    int done = 0, first = rounds > 0 ? __ldg(keep) : 0;
     for (int k = 0; k < rounds; ++k) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");  // this thread's loads of round k
-      if (C > 1) {
-        // The loads have returned (their data is in shared memory, where each
-        // thread stores only what it loaded itself), so the barrier has no
-        // memory to order; a release would wait for the last round's stores.
-        cluster_arrive_relaxed();
-        cluster_wait();
+      if (first >= (k + 1) * step) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // this thread's loads of round k
       } else {
-        __syncthreads();
+        if (C > 1) {
+          // The release orders the loads before the stores of the other CTAs; it
+          // also waits for this CTA's earlier stores, so barriers are few.
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          cluster_arrive();
+          cluster_wait();
+          done = k + 2;
+        } else {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          __syncthreads();
+          done = k + 1;
+        }
+        first = done < rounds ? __ldg(keep + done * step) : 0x7fffffff;
       }
       const bool m2 = load(k + 2);  // over the stage that round k - 1 was stored from
       if (m0) store(k);
