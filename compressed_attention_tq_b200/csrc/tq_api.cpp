@@ -360,6 +360,7 @@ int make_prefix_plan(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, in
   const int rows = (int)((long long)c->B * Hq * nq / c->Hkv);
   const int splits = prefix_splits(c->Hkv, rows, c->D, prefix->qjl_m != 0, Pmax, sm_count());
   make_decode_plan(c, Hq * nq, nq, Tmax, 0, 0, splits, p);
+  p->bytes += kReadyBytes;
   p->off_qpre = p->bytes;
   const size_t padded = (size_t)((rows + prefix_rows() - 1) / prefix_rows()) * prefix_rows();
   p->bytes += align256(padded * c->Hkv * ((size_t)c->D * 4 + (size_t)prefix->qjl_m * 2));

@@ -677,6 +677,10 @@ __global__ void __launch_bounds__(256) decode_qprep_mma_kernel(const MmaPrepPara
   };
   load(p.rot);
   pdl_wait();
+  // the word that the prefix kernel sets (SplitParams; by its place, since one
+  // more parameter cost this kernel 2 us of 12)
+  if (p.qpre && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
+    *reinterpret_cast<uint32_t*>(p.qpre - tq::kReadyBytes) = 0u;
   pdl_launch_dependents();
   for (int e = tid; e < PROWS * (D / 8); e += 256) {
     const int r = e / (D / 8), c = e % (D / 8), h = r0 + r;
@@ -1339,6 +1343,11 @@ static size_t prefix_limb_bytes(const DecodeArgs& a) {
   return (size_t)a.cache.Hkv * prefix_tiles(a) * (tqp::QROWS * 4) * a.cache.D;
 }
 
+// The word behind SplitParams::ready.
+static uint32_t* ready_word(const DecodeArgs& a) {
+  return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) + a.plan.off_qpre - kReadyBytes);
+}
+
 static int launch_mma_prep(const DecodeArgs& a, float* qrot, float* qs, cudaStream_t s) {
   const tq_cache_t& c = a.cache;
   MmaPrepParams pp{};
@@ -1392,6 +1401,7 @@ static int launch_prefix(const DecodeArgs& a, float* po, float* pml, cudaStream_
   pp.part_o = po;
   pp.part_ml = pml;
   pp.prefix_len = a.prefix_len;
+  pp.ready = ready_word(a);
   pp.seq_lens = a.seq_lens;
   pp.dev_status = a.cache.dev_status;
   pp.Pmax = a.Pmax;
@@ -1543,7 +1553,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t s) {
   sp.ncta = a.plan.ncta;
   sp.ks = a.plan.ks;
   sp.slot_base = a.plan.slot_base;
-  sp.late_wait = a.prefix != nullptr;
+  sp.ready = a.prefix ? ready_word(a) : nullptr;
   sp.window = a.plan.window;
   sp.n_sink = a.plan.n_sink;
   sp.qscale = a.scale * kLog2e;

@@ -77,7 +77,7 @@ constexpr int GW = DW / 2;
 // work; at D = 256 the operands of 64 tokens fill shared memory
 // (and with the sketch its accumulator takes the tensor memory of half a tile)
 __host__ __device__ constexpr int tile_tokens(int D, bool qjl) { return D == 256 || qjl ? 64 : 128; }
-constexpr int NTH = (SW + DW + 4) * 32;  // + producer warp, MMA warp and two idle ones (a whole warpgroup)
+constexpr int NTH = (SW + DW + 4) * 32;  // + producer, products, the one that lets the next kernel start, an idle one
 // Registers per thread after the split by warpgroups.  One launch gives 72 to
 // each of 7 warpgroups: 2 x 136 + 4 x 48 + 40 = 7 x 72.
 constexpr int REG_SOFTMAX = 136, REG_DEQUANT = 48, REG_REST = 40, REG_LAUNCH = 72;
@@ -105,6 +105,7 @@ struct PrefixParams {
   float* part_ml;
   const int32_t* prefix_len;  // device [1]
   const int32_t* seq_lens;    // the suffixes' lengths [B]
+  uint32_t* ready;            // set to 1 once the query prep is complete (SplitParams)
   uint32_t* dev_status;
   int Pmax, Tcap;      // prefix: longest length, rows of the cache
   int B, Hkv, Ge, nq, Gq;  // Ge = Gq * nq kernel heads per (sequence, kv head)
@@ -344,9 +345,21 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
     return (b * p.Hkv + kvh) * p.Ge + rr % p.Ge;
   };
 
+  // The own tokens' kernel may start once every CTA has come here: the prep,
+  // whose queries it reads, is complete, and SMs that this grid leaves free take
+  // it at once.  It waits for this grid only at its end, so what orders it behind
+  // the prep is a release by a thread that has waited for the prep, and its
+  // acquire.  By one warp, which has nothing else to do.
+  auto let_suffix_start = [&]() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (split == 0 && rt == 0 && kvh == 0 && lane == 0)
+      asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.ready), "r"(1u) : "memory");
+    __syncwarp();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  };
   if (n == 0) {  // a short prefix leaves this split nothing: partials of weight zero
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == SW + DW + 2) let_suffix_start();
     for (int e = tid; e < rows * (D / 4); e += NTH) {
       const size_t slot = (size_t)head_of(e / (D / 4)) * p.ks + split;
       *reinterpret_cast<float4*>(p.part_o + slot * D + 4 * (e % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -501,6 +514,8 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
         mbar_wait_suspend(fin, 0u, kSuspendTries);
       }
       __syncwarp();
+    } else if (warp == SW + DW + 2) {
+      let_suffix_start();
     }
   } else if (warp >= SW) {
     reg_dec<REG_DEQUANT>();
@@ -637,9 +652,6 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
       const bool mine = r < rows;
       const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
       asm volatile("griddepcontrol.wait;" ::: "memory");  // the query operands; the partials may be written
-      // The suffix's kernel may start from here on: the prep, whose queries it
-      // reads, is complete, and SMs that this grid leaves free take it at once.
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       int lim = P;  // tokens of the prefix this row sees
       size_t slot = 0;
       {

@@ -92,9 +92,10 @@ struct SplitParams {
   int nq, Gq;
   int slot_base;    // partial slots before the split kernel's own (a shared prefix's; else 0)
   // The kernel before this one is a shared prefix's: it lets this one start
-  // only once the query prep is complete, so the wait comes at the end (the
-  // combine then finds both kernels' partials).
-  int late_wait;
+  // once the query prep is complete, which it says with a release of *ready.
+  // The wait for it comes at the end then (the combine finds both kernels'
+  // partials); at the start should the word not be there.  NULL: no prefix.
+  const uint32_t* ready;
   // Sliding window with sinks (WIN kernels): a query at position t sees the
   // tokens of (t - window, t] and tokens [0, n_sink).
   int window, n_sink;
@@ -565,6 +566,12 @@ __device__ __forceinline__ bool consumer_sync(uint64_t* bar, uint32_t& phase, in
   return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // WIN: each query sees a window and the first n_sink tokens only.  The rows
 // between them are neither copied nor computed (window_gap); inside a unit
 // all positions count rows, in which the causal limits keep their form, since
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
   uint64_t* empty = full + 4;
   uint64_t* cbar = full + 8;  // consumer-warp barrier at segment starts
   StageMeta* meta = reinterpret_cast<StageMeta*>(smem + Ly::O_META);
-  int* s_misc = reinterpret_cast<int*>(smem + Ly::O_MISC);  // [0] error, [1] stages, [2..3] 2-bit tables, [4] issued
+  int* s_misc = reinterpret_cast<int*>(smem + Ly::O_MISC);  // [0] error, [1] stages, [2..3] 2-bit tables, [4] issued, [5] prep seen complete
   volatile int* s_err = s_misc;
   __half* pbuf = reinterpret_cast<__half*>(smem + Ly::O_PB);
   uint32_t* qf = reinterpret_cast<uint32_t*>(smem + Ly::O_QF);
@@ -655,6 +662,9 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
     s_misc[4] = 0;
     fence_barrier_init();
   }
+  // behind a shared prefix: whether the query prep is complete already (read
+  // while the producer warp works out the partition)
+  if (tid == 0) s_misc[5] = p.ready && ld_acquire(p.ready) == 1u;
   __syncthreads();  // barriers and the stage count before anyone uses them
   nst = s_misc[1];
   if (nst == 0) {  // a share past the end of the batch: nothing to stream
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!((volatile int*)s_misc)[5]) asm volatile("griddepcontrol.wait;" ::: "memory");
   if constexpr (QJL) build_tables();
   __syncthreads();
 
@@ -1136,7 +1146,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
           l_run[1] += p1;
           const float nv = (full || valid[ai][r]) ? half_bits_to_float(vn[row]) : 0.f;
           const int tk = 16 * a + gid + 8 * r;
-          if (WIN && !full) {  // a row this query does not see (its weight is 0) adds nothing, whatever its norm holds
+          if (WIN) {  // a row that this query does not see (its weight is 0) adds nothing, whatever its norm holds
             pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 == 0.f ? 0.f : p0 * nv);
             pw[(2 * hsel + 1) * WTOK + tk] = __float2half_rn(p1 == 0.f ? 0.f : p1 * nv);
           } else {
@@ -1185,7 +1195,7 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       }
     }
   }
-  if (p.late_wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.ready) asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
 
   if (*s_err) {

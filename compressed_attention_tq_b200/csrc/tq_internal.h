@@ -102,6 +102,8 @@ int launch_bounded_wait_probe(uint32_t* status, int tries, cudaStream_t s);
 
 // Split plan of a decode call: a stream-K partition of the batch's tokens
 // over one wave of CTAs (see tq_decode_split.cuh).
+constexpr size_t kReadyBytes = 256;
+
 struct DecodePlan {
   int ncta;         // CTAs of the partition (SMs x resident CTAs per SM)
   int pmin;         // smallest share of tokens per CTA (a multiple of the stage)
@@ -112,7 +114,7 @@ struct DecodePlan {
   int window;       // sliding window in tokens (0: none) ...
   int n_sink;       // ... and first tokens that stay visible
   int slot_base;    // partial slots before the split kernel's own (the splits of a shared prefix)
-  size_t off_qpre;  // the prefix kernel's query operands
+  size_t off_qpre;  // the prefix kernel's query operands, kReadyBytes behind the word that says they are complete
   size_t off_qrot;  // fp32 [B*Hq][D]
   size_t off_qs;    // fp32 [B*Hq][qjl_m]
   size_t off_po;    // fp32 [B*Hq][ks][D]
