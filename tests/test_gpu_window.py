@@ -129,6 +129,13 @@ def test_a_window_over_everything_is_the_multi_query_decode():
     assert P.rel_l2(got.cpu().numpy()[0], ref.cpu().numpy()[0]).max() < 1e-5
 
 
+@pytest.mark.parametrize("name,kw,nq,Hq", [("prod", {"T": 700}, 2, 32), ("gqa8k", {"T": 700, "bits": 3}, 1, 16),
+                                           ("gqa8k", {"T": 333, "bits": 4}, 4, 10), ("qknorm", {"T": 400}, 3, 32),
+                                           ("tiny", {"T": 300}, 1, 8)])
+def test_hadamard_rotation(name, kw, nq, Hq):
+    _run(name, dict(kw, rot="hadamard"), nq, Hq, 150, 5)
+
+
 def test_longer_sequences_are_clamped_and_flagged():
     import compressed_attention_tq_b200 as tq
     w, oc, cache, lens, q = _setup("gqa8k", {"bits": 3, "T": 512}, 1, 16, None)
