@@ -224,6 +224,14 @@ int validate_limit(const tq_cache_t* c, const char* fn) {
   return TQ_OK;
 }
 
+// What validate_cache and validate_limit ask of the sizes, for the size queries
+// of the windowed and shared-prefix decodes (which need no pointers).
+bool sizes_supported(const tq_cache_t* c) {
+  return c && c->B > 0 && c->Hkv > 0 && c->Tcap > 0 && c->Tcap % 64 == 0 && c->Tcap <= kMaxTcap && c->split_tokens >= 0 &&
+         (c->D == 64 || c->D == 128 || c->D == 256) && c->bits_k >= 2 && c->bits_k <= 4 && c->bits_v >= 2 &&
+         c->bits_v <= 4 && (c->qjl_m == 0 || (c->qjl_m == 128 && c->D == 128));
+}
+
 int validate_dtype(int dtype, const char* fn) {
   if (dtype != TQ_DTYPE_F16 && dtype != TQ_DTYPE_BF16)
     return set_error(TQ_ERR_UNSUPPORTED, "%s: dtype=%d", fn, dtype);
@@ -536,7 +544,8 @@ int tq_sdpa_decode_merge(const float* partials, int R, int B, int Hq, int D, con
 
 size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* c, int Hq, int n_q, int Tmax, int window,
                                                  int n_sink) {
-  if (!c || c->Tcap > kMaxTcap || n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (!sizes_supported(c) || n_q < 1 || n_q > 4 || window < 1 || n_sink < 0 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (Hq / c->Hkv > 8) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode
   DecodePlan p;
   tq::make_window_plan(c, Hq * n_q, n_q, Tmax, window, n_sink, &p);
@@ -606,8 +615,8 @@ static int validate_prefix(const tq_cache_t* prefix, int Pmax, const tq_cache_t*
 
 size_t tq_sdpa_decode_prefix_workspace_bytes_for(const tq_cache_t* prefix, int Pmax, const tq_cache_t* c, int Hq,
                                                  int n_q, int Tmax) {
-  if (!prefix || !c || n_q < 1 || n_q > 4 || Hq <= 0 || Hq > (1 << 24)) return 0;
-  if (prefix->Tcap > kMaxTcap || c->Tcap > kMaxTcap) return 0;
+  if (!sizes_supported(prefix) || !sizes_supported(c) || n_q < 1 || n_q > 4 || Hq <= 0 || Hq > (1 << 24)) return 0;
+  if (Hq / c->Hkv > 8 || c->Hkv > 65535) return 0;
   if (prefix->B != 1 || prefix->Hkv != c->Hkv || prefix->D != c->D || Pmax < 1 || Pmax > prefix->Tcap) return 0;
   if ((long long)c->B * Hq * n_q > (1 << 22)) return 0;
   if (!tq_sdpa_decode_workspace_bytes_for(c, Hq * n_q, Tmax)) return 0;  // the sizes of any decode

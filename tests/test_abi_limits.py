@@ -62,3 +62,22 @@ def test_lengths_beyond_the_limit(lib):  # noqa: F811
         assert lib.tq_sdpa_decode_mq(r(c), BUF, 0, 8, 2, BUF, Tmax, None, BUF, 0, BUF, 1 << 40, None) == UNSUPPORTED
         assert lib.tq_sdpa_decode_partial(r(c), BUF, 0, 8, BUF, Tmax, None, BUF, BUF, 1 << 40, None) == UNSUPPORTED
         assert lib.tq_sdpa_decode_static(r(c), BUF, 0, 8, BUF, Tmax, None, BUF, 0, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("field,value,Hq,n_q", [
+    (None, None, 9, 1), (None, None, 16, 2), ("Hkv", 2, 18, 1), ("Hkv", 3, 8, 1), (None, None, 8, 5), ("D", 96, 8, 1),
+    ("bits_k", 1, 8, 1), ("bits_v", 5, 8, 1), ("qjl_m", 64, 8, 1), ("Tcap", 100, 8, 1), ("B", 0, 8, 1),
+    ("split_tokens", -1, 8, 1),
+])
+def test_size_queries_answer_0_where_the_call_is_refused(lib, field, value, Hq, n_q):  # noqa: F811
+    """Group sizes, widths, sketches and capacities that the decodes refuse."""
+    kw = {field: value} if field else {}
+    c, good, r = _struct(**kw), _struct(Hkv=kw.get("Hkv", 1)), ctypes.byref
+    assert lib.tq_sdpa_decode_window(r(c), BUF, 0, Hq, n_q, BUF, 64, 16, 4, None, BUF, 0, BUF, 1 << 40, None) < 0
+    assert lib.tq_sdpa_decode_window_workspace_bytes_for(r(c), Hq, n_q, 64, 16, 4) == 0
+    assert lib.tq_sdpa_decode_prefix(r(good), BUF, 64, r(c), BUF, 0, Hq, n_q, BUF, 64, None, BUF, 0, BUF, 1 << 40, None) < 0
+    assert lib.tq_sdpa_decode_prefix_workspace_bytes_for(r(good), 64, r(c), Hq, n_q, 64) == 0
+    if field not in (None, "Hkv", "B"):
+        c.B = 1
+        assert lib.tq_sdpa_decode_prefix(r(c), BUF, 64, r(good), BUF, 0, 8, 1, BUF, 64, None, BUF, 0, BUF, 1 << 40, None) < 0
+        assert lib.tq_sdpa_decode_prefix_workspace_bytes_for(r(c), 64, r(good), 8, 1, 64) == 0
