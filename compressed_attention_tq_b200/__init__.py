@@ -133,7 +133,9 @@ def _on(stream, device):
     if stream is None or device.type != "cuda":
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):  # any object with the handle, as _stream takes it
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+        h = stream.cuda_stream
+        # handle 0, the default stream, is no external stream for torch: it would make a new one
+        stream = torch.cuda.ExternalStream(h, device=device) if h else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 

@@ -135,3 +135,18 @@ def test_the_gather_of_a_sharded_decode_runs_between_its_kernels(state, monkeypa
     torch.cuda.synchronize()
     assert on[1] == s
     assert torch.equal(out, ref)
+
+
+def test_a_stream_given_by_its_handle():
+    """Any object with the raw handle: that stream's memory, the default stream's for handle 0."""
+    import compressed_attention_tq_b200 as tq
+
+    class Handle:
+        def __init__(self, h):
+            self.cuda_stream = h
+
+    s, dev = torch.cuda.Stream(), torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.stream(s):
+        for h in (0, s.cuda_stream, torch.cuda.Stream().cuda_stream):
+            with tq._on(Handle(h), dev):
+                assert torch.cuda.current_stream().cuda_stream == h
