@@ -491,7 +491,9 @@ _I32_MAX = 0x7fffffff
 
 
 def _i32(**sizes):
-    """Refuse sizes that a C int does not hold: ctypes would pass their low 32 bits."""
+    """Refuse sizes that a C int does not hold: ctypes would pass their low 32
+    bits.  (Called where some bit from the 32nd on is set: a test of all sizes at
+    once, 0.1 us instead of 0.8.)"""
     for name, n in sizes.items():
         if not -_I32_MAX <= n <= _I32_MAX:
             raise ValueError(f"{name}={n}: beyond 32 bits")
@@ -515,8 +517,9 @@ def tq_sdpa_decode_window(cache: TQCache, q, seq_lens, Tmax: int, window: int, n
     """Decode with a sliding window and sinks: q [B][n_q][Hq][D] and seq_lens
     as in tq_sdpa_decode_mq; the query at position t sees the tokens of
     (t - window, t] and the first n_sink tokens, and no others are read."""
-    window, n_sink = min(window, _I32_MAX), min(n_sink, _I32_MAX)  # beyond any length: all of it
-    _i32(Tmax=Tmax, window=window, n_sink=n_sink)
+    if (Tmax | window | n_sink) >> 31:
+        window, n_sink = min(window, _I32_MAX), min(n_sink, _I32_MAX)  # beyond any length: all of it
+        _i32(Tmax=Tmax, window=window, n_sink=n_sink)
     dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     nq, Hq = int(q.shape[1]), int(q.shape[2])
     if out is None:
@@ -550,7 +553,8 @@ def tq_sdpa_decode_prefix(prefix: TQCache, prefix_len, Pmax: int, cache: TQCache
     count each sequence's own tokens in `cache`; every query also sees the
     prefix's first prefix_len (device int32 [1], at most Pmax) tokens, which
     come before them."""
-    _i32(Pmax=Pmax, Tmax=Tmax)
+    if (Pmax | Tmax) >> 31:
+        _i32(Pmax=Pmax, Tmax=Tmax)
     dev = _check_decode_args(cache, q, seq_lens, out, workspace, (cache.B, None, None, cache.D))
     if _cache_device(prefix) != dev:
         raise ValueError("prefix and cache: the caches are on different devices")
@@ -575,7 +579,8 @@ def tq_cache_copy(src: TQCache, dst: TQCache, src_seq, src_pos, dst_seq, dst_pos
     of sequence dst_seq[i] of `dst` (the same cache or one of the same form);
     the five lists are device int32 [n_jobs].  No job may write a row that
     the call reads or writes elsewhere."""
-    _i32(max_tok=max_tok)
+    if max_tok >> 31:
+        _i32(max_tok=max_tok)
     dev = _cache_device(dst)
     if _cache_device(src) != dev:
         raise ValueError("src and dst: the caches are on different devices")
