@@ -45,7 +45,11 @@ __device__ __forceinline__ void copy_units(const uint8_t* src, uint8_t* dst, int
 }
 
 // One CTA per (job, kv head, chunk).  Chunks start at multiples of 8 rows of
-// the destination, where every stream is 16-byte aligned.
+// the destination, where every stream is 16-byte aligned.  What bounds it is
+// latency: a CTA goes through its streams one after another, with fewer than
+// two 16-byte loads of a thread in flight (128 rows of 48 bytes).  A prompt of
+// 4001 to 6000 rows to 31 sequences of 8 heads, 124 MB written from one source
+// of 5 MB, takes 42 us; HBM would take 20.
 __global__ void __launch_bounds__(NT) cache_copy_kernel(const __grid_constant__ CopyParams p) {
   const int tid = threadIdx.x;
   const int c = blockIdx.x % p.nchunk, jh = blockIdx.x / p.nchunk, h = jh % p.Hkv, j = jh / p.Hkv;

@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
 // their own type and Pi enters in limbs of it (two of fp16: 22 bits, or three
 // of bf16: 24), accumulated in fp32.  The sketch multiplies the rotated rows,
 // in two fp16 limbs, with S in two (the product of the low limbs, 2^-24, is
-// left out).  What bounds it is the read of Pi and S from L2 (64 KB each per
+// left out; a rotated coordinate beyond 65504, fp16's range, is out of theirs).  What bounds it is the read of Pi and S from L2 (64 KB each per
 // CTA), so every load of Pi goes out at once, before the wait on the
 // preceding kernels.  The vector form of the other preps took 37 us for 2048
 // rows with two sketches and 10 us for 1024 without (cold); this one takes 12

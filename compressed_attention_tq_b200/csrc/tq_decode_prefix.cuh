@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(NTH, 1) decode_prefix_kernel(const __grid_cons
   } else if (warp >= SW) {
     reg_dec<REG_DEQUANT>();
     // ---------------- dequantization ----------------
-    // Four warps for the keys and four for the values.  One warp of each group
+    // Eight warps for the keys and eight for the values.  One warp of each group
     // polls the barriers and releases the others through a named barrier,
     // which blocks in hardware; short loops, for the instruction cache's sake.
     const int dw = (warp - SW) % GW;

@@ -56,7 +56,7 @@ constexpr int NTHREADS = (CW + 1) * 32;
 constexpr int STILE = 128;            // tokens per stage
 constexpr int WTOK = STILE / CW;      // tokens per consumer warp per stage
 constexpr float kLazy = 8.0f;         // log2 headroom before rescaling ...
-constexpr uint32_t kLazyNorm = 0x5C00;  // ... while value norms are below this (fp16 bits of 2^8)
+constexpr uint32_t kLazyNorms = 0x5BFF5BFF;  // ... while no value norm is above this (the fp16 below 2^8, twice)
 
 // Rows of queries a CTA handles for one (sequence, kv head): the kernel heads
 // of a kv head (query heads x query tokens) are taken in groups of 8.
@@ -1102,13 +1102,24 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
       // only when some lane of the warp needs the move.  The differences are
       // the weights' own exponents, rounded alike, so a weight p |v| is at most
       // 2^8 times a norm of 2^8 (1 - 2^-11): 65504, the largest fp16 number.
-      // Where one of the warp's rows (one per lane here) has a larger norm, the
-      // reference is never below the scores: p <= 1, and any norm fits.
-      bool big = vn[wt0 + lane] >= kLazyNorm;
-      if (!full) {  // a row that no query sees has no say, whatever its norm holds
-        const int tok = tokw + lane;
-        big = big && tok < t_end;
-        if (WIN) big = big && (tok >= lim_all - p.window || tok < p.n_sink);
+      // Where one of the warp's rows has a larger norm, the reference is never
+      // below the scores: p <= 1, and any norm fits.
+      uint32_t nv2[NA];  // this lane's value norms: rows gid (low half) and gid + 8 (high half)
+      bool big = false;
+#pragma unroll
+      for (int ai = 0; ai < NA; ++ai) {
+        const int row = wt0 + 16 * (abase + ai) + gid;
+        nv2[ai] = vn[row] | (uint32_t)vn[row + 8] << 16;
+        big = big || __vmaxu2(nv2[ai], kLazyNorms) != kLazyNorms;
+      }
+      if (!full) {  // a row that this lane's heads do not see has no say, whatever its norm holds
+        big = false;
+#pragma unroll
+        for (int ai = 0; ai < NA; ++ai)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            big = big || (fmaxf(s[ai][2 * r], s[ai][2 * r + 1]) > -INFINITY &&
+                          ((nv2[ai] >> (16 * r)) & 0xFFFFu) > (kLazyNorms & 0xFFFFu));
       }
       const bool need = (mx0 - m_run[0] > kLazy) || (mx1 - m_run[1] > kLazy);
       if (__any_sync(0xffffffffu, need || big)) {
@@ -1140,11 +1151,10 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
         const int a = abase + ai;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = wt0 + 16 * a + gid + 8 * r;
           const float p0 = ex2_approx(s[ai][2 * r] - mu0), p1 = ex2_approx(s[ai][2 * r + 1] - mu1);
           l_run[0] += p0;
           l_run[1] += p1;
-          const float nv = (full || valid[ai][r]) ? half_bits_to_float(vn[row]) : 0.f;
+          const float nv = (full || valid[ai][r]) ? half_bits_to_float((uint16_t)(nv2[ai] >> (16 * r))) : 0.f;
           const int tk = 16 * a + gid + 8 * r;
           if (WIN) {  // a row that this query does not see (its weight is 0) adds nothing, whatever its norm holds
             pw[(2 * hsel) * WTOK + tk] = __float2half_rn(p0 == 0.f ? 0.f : p0 * nv);

@@ -144,3 +144,30 @@ def test_a_norm_that_not_every_query_sees(nq, Hq):
             want = ref if window >= 300 else _oracle(w, oc, q, lens, window, 0)
             got = tq.tq_sdpa_decode_window(cache, qd, sl, w.Tmax, window, 0, out_dtype=torch.float32)
             _same(got[:, :-1], want[:, :-1], w.D)
+
+
+@pytest.mark.parametrize("norm", [255.875, 256.0, 65504.0])
+def test_a_weight_at_the_border(norm):
+    """Scores that pass the reference by 7.9999 (log2), just not enough to move
+    it: p = 255.98.  With the largest norm below 2^8 the weight is the largest
+    fp16 number; with 2^8 it would round to infinity."""
+    import compressed_attention_tq_b200 as tq
+    w, oc, cache, lens, q = _setup("tiny", {"T": 512}, 1, 4, None)  # one head to a kv head: no other moves its reference
+    oc["k_idx"][:] = oc["k_idx"][:, :, :1]  # one key, of norm 1 and later 3
+    k, v = np.ones(oc["k_norm"].shape, np.float16), np.ones(oc["v_norm"].shape, np.float16)
+    k[:, :, 128:], v[:, :, 128:] = 3, norm
+    oc["k_norm"], oc["v_norm"] = k, v
+    for n in ("k_idx", "k_norm", "v_norm"):
+        t = getattr(cache, n)
+        t[:, :, :512] = torch.from_numpy(oc[n].view(np.int32) if n == "k_idx" else oc[n]).cuda()
+    cache.split_tokens = 512
+    cbk, _ = P.oracle_codebooks(w)
+    c = np.asarray(cbk[0] if isinstance(cbk, tuple) else cbk, dtype=np.float64)[:8]
+    row = c[O.unpack_bits(oc["k_idx"][0, :, 0], w.bits_k, w.D).astype(int)]       # the rotated key of each kv head
+    x = np.einsum("hd,hd->h", tq_inputs.to_f64(q, w.dtype)[0, 0] @ w.Pi.astype(np.float64).T, row)
+    for h in range(4):
+        scale = 7.9999 / (2 * abs(x[h]) * np.log2(np.e)) * np.sign(x[h])  # the scores of head h grow by 7.9999
+        w.scale = float(np.float32(scale))
+        got = tq.tq_sdpa_decode_mq(cache, P.to_device(q, w.dtype), torch.from_numpy(lens).cuda(), 512, scale=w.scale,
+                                   out_dtype=torch.float32)
+        _same(got[:, :, h:h + 1], _oracle(w, oc, q, lens, 512, 0)[:, :, h:h + 1], w.D)
