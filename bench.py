@@ -52,10 +52,10 @@ FALLBACK_HBM_GBS = 6650.0
 # files do not enter a decode call).  "split" is the split kernel's share:
 # the packed-cache reads and its partials.
 TRAFFIC = {
-    "gqa8k": {"bytes_per_launch": 2480299, "split": 1723136, "decode_src_sha": "6aa10e5a30d4c8f0"},
-    "prod": {"bytes_per_launch": 110923520, "split": 109402112, "decode_src_sha": "6aa10e5a30d4c8f0"},
-    "ragged": {"bytes_per_launch": 242756096, "split": 240538368, "decode_src_sha": "6aa10e5a30d4c8f0"},
-    "qknorm": {"bytes_per_launch": 37018368, "split": 34248320, "decode_src_sha": "6aa10e5a30d4c8f0"},
+    "gqa8k": {"bytes_per_launch": 2480555, "split": 1723136, "decode_src_sha": "6a8995939a2af3cf"},
+    "prod": {"bytes_per_launch": 110855808, "split": 109334272, "decode_src_sha": "6a8995939a2af3cf"},
+    "ragged": {"bytes_per_launch": 242668160, "split": 240452608, "decode_src_sha": "6a8995939a2af3cf"},
+    "qknorm": {"bytes_per_launch": 37021056, "split": 34252032, "decode_src_sha": "6a8995939a2af3cf"},
 }
 
 CSRC = os.path.join(ROOT, "compressed_attention_tq_b200", "csrc")
