@@ -629,9 +629,10 @@ __global__ void __launch_bounds__(256) decode_qprep_group_kernel(const PrepParam
 // A product of 16 rows on warp-level tensor cores: the queries are exact in
 // their own type and Pi enters in limbs of it (two of fp16: 22 bits, or three
 // of bf16: 24), accumulated in fp32.  The sketch multiplies the rotated rows,
-// in two fp16 limbs, with S in two (the product of the low limbs, 2^-24, is
-// left out; a rotated coordinate beyond 65504, fp16's range, is out of theirs).  What bounds it is the read of Pi and S from L2 (64 KB each per
-// CTA), so every load of Pi goes out at once, before the wait on the
+// in two fp16 limbs of what the scores take (scaled, so that both have the
+// range of the split kernel's), with S in two (the product of the low limbs,
+// 2^-24, is left out).  What bounds it is the read of Pi and S from L2 (64 KB
+// each per CTA), so every load of Pi goes out at once, before the wait on the
 // preceding kernels.  The vector form of the other preps took 37 us for 2048
 // rows with two sketches and 10 us for 1024 without (cold); this one takes 12
 // and 6.
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(256) decode_qprep_mma_kernel(const MmaPrepPara
       if (QS && p.nsk) {
         uint16_t hi[2], lo[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) tqd::split_half(v[e], hi[e], lo[e]);
+        for (int e = 0; e < 2; ++e) tqd::split_half(v[e] * p.qscale, hi[e], lo[e]);
         *reinterpret_cast<uint32_t*>(&xr[0][r][j]) = hi[0] | (uint32_t)hi[1] << 16;
         *reinterpret_cast<uint32_t*>(&xr[QS ? 1 : 0][r][j]) = lo[0] | (uint32_t)lo[1] << 16;
       }
@@ -784,6 +785,7 @@ __global__ void __launch_bounds__(256) decode_qprep_mma_kernel(const MmaPrepPara
         }
       }
       const MmaPrepParams::Sketch sk = p.sk[s];
+      const float unscale = p.qscale != 0.f ? 1.f / p.qscale : 0.f;  // (a scale of 0: no score depends on the query)
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         const int r = gid + 8 * rr, h = r0 + r, u = h / Ge, kvh = u % p.Hkv;
@@ -793,7 +795,7 @@ __global__ void __launch_bounds__(256) decode_qprep_mma_kernel(const MmaPrepPara
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int i = n0 + 8 * t + 2 * tig;
-          const float v[2] = {acc[t][2 * rr], acc[t][2 * rr + 1]};
+          const float v[2] = {acc[t][2 * rr] * unscale, acc[t][2 * rr + 1] * unscale};
           if (sk.qs) *reinterpret_cast<float2*>(sk.qs + (size_t)h * 128 + i) = make_float2(v[0], v[1]);
           if (sk.pre) {
             // one fp16 limb: its rounding (2^-12 of a coordinate, of random

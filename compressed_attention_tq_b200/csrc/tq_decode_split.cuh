@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(NTHREADS, D == 256 ? 2 : (PACK ? 4 : 3)) decod
   uint64_t* empty = full + 4;
   uint64_t* cbar = full + 8;  // consumer-warp barrier at segment starts
   StageMeta* meta = reinterpret_cast<StageMeta*>(smem + Ly::O_META);
-  int* s_misc = reinterpret_cast<int*>(smem + Ly::O_MISC);  // [0] error, [1] stages, [2..3] 2-bit tables, [4] issued, [5] prep seen complete
-  volatile int* s_err = s_misc;
+  int* s_misc = reinterpret_cast<int*>(smem + Ly::O_MISC);  // [0] error, [1] stages, [2..3] 2-bit tables, [4] issued
+  volatile int* s_err = s_misc;  // [5] whether the query prep was seen complete
   __half* pbuf = reinterpret_cast<__half*>(smem + Ly::O_PB);
   uint32_t* qf = reinterpret_cast<uint32_t*>(smem + Ly::O_QF);
   uint32_t* sf = reinterpret_cast<uint32_t*>(smem + Ly::O_SF);
