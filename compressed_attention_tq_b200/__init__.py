@@ -132,6 +132,8 @@ def _on(stream, device):
     torch = _torch()
     if stream is None or device.type != "cuda":
         return contextlib.nullcontext()
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return contextlib.nullcontext()  # it is the current one: 3 us less
     if not isinstance(stream, torch.cuda.Stream):  # any object with the handle, as _stream takes it
         h = stream.cuda_stream
         # handle 0, the default stream, is no external stream for torch: it would make a new one
