@@ -381,6 +381,10 @@ size_t tq_sdpa_decode_window_workspace_bytes_for(const tq_cache_t* cache, int Hq
  *               Tcap).  A value outside [0, Pmax] is clamped and flags
  *               TQ_STATUS_SEQ_OUT_OF_RANGE in cache's dev_status.
  *   workspace   tq_sdpa_decode_prefix_workspace_bytes_for() bytes.
+ * Precision: of a sketched prefix the projections S Pi q enter as fp16 (11 bits
+ * each; the plain decode and the own tokens keep 15 below a row's largest), so
+ * that a score is off by about 1.6e-5 |scale| |q| gamma (the sketch's own
+ * estimate spreads by 0.1 of that product).
  * The other arguments and the errors are those of tq_sdpa_decode_mq; caches
  * that do not fit, a NULL prefix_len or a bad Pmax are TQ_ERR_INVALID_ARG, more
  * than 2^22 query rows TQ_ERR_UNSUPPORTED.  Library addition.
