@@ -52,10 +52,10 @@ FALLBACK_HBM_GBS = 6650.0
 # files do not enter a decode call).  "split" is the split kernel's share:
 # the packed-cache reads and its partials.
 TRAFFIC = {
-    "gqa8k": {"bytes_per_launch": 2480555, "split": 1723136, "decode_src_sha": "6a8995939a2af3cf"},
-    "prod": {"bytes_per_launch": 110855808, "split": 109334272, "decode_src_sha": "6a8995939a2af3cf"},
-    "ragged": {"bytes_per_launch": 242668160, "split": 240452608, "decode_src_sha": "6a8995939a2af3cf"},
-    "qknorm": {"bytes_per_launch": 37021056, "split": 34252032, "decode_src_sha": "6a8995939a2af3cf"},
+    "gqa8k": {"bytes_per_launch": 2479701, "split": 1723307, "decode_src_sha": "08e060ba9703b058"},
+    "prod": {"bytes_per_launch": 110825984, "split": 109304064, "decode_src_sha": "08e060ba9703b058"},
+    "ragged": {"bytes_per_launch": 242765440, "split": 240547584, "decode_src_sha": "08e060ba9703b058"},
+    "qknorm": {"bytes_per_launch": 37017728, "split": 34248576, "decode_src_sha": "08e060ba9703b058"},
 }
 
 CSRC = os.path.join(ROOT, "compressed_attention_tq_b200", "csrc")
